@@ -75,7 +75,9 @@
  *   PA_STATUS_BAD_SEQ_LEN   seq_lens[b] < 0 or > max_blocks_per_seq *
  *                           block_size; the length is clamped into range;
  *   PA_STATUS_TIMEOUT       a bounded wait for a shared-memory copy gave up
- *                           (after about a second) instead of hanging.
+ *                           (after about a second) instead of hanging;
+ *   PA_STATUS_BAD_POSITION  (appends) a new token's position is past the end
+ *                           of the cosine and sine table; it is not written.
  * The caller reads *status after synchronising the stream.
  * Entry points are thread-safe; the only global state is a per-device
  * cache of the multiprocessor count and of the kernels' shared-memory
@@ -110,7 +112,8 @@ enum {
 enum {
     PA_STATUS_BAD_BLOCK_ID = 1,
     PA_STATUS_BAD_SEQ_LEN = 2,
-    PA_STATUS_TIMEOUT = 4
+    PA_STATUS_TIMEOUT = 4,
+    PA_STATUS_BAD_POSITION = 8
 };
 
 /*
@@ -407,6 +410,134 @@ PA_API int pa_set_rows_kernel(int mode);
  * counterpart in the method's description.
  */
 PA_API int pa_set_merge_form(int form);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Filling a paged cache, and attention over a cache held in 8 bits.  The
+ * method's description reads caches that something else has filled and holds
+ * them in 16 bits; these entry points have no counterpart there.
+ * ---------------------------------------------------------------------------
+ *
+ * The 8-bit cache.  key_cache and value_cache are [num_blocks, num_kv_heads,
+ * block_size, head_dim] as above, of e4m3 codes (1 byte: sign, 4 exponent
+ * bits, 3 mantissa bits; largest value 448; the two codes with all other bits
+ * set are NaN).  k_scales and v_scales are [num_blocks, num_kv_heads] float32:
+ * a code stands for its e4m3 value times the scale of its block and KV head.
+ * Scales are finite and not negative.
+ */
+
+/*
+ * Writes the keys and values of new tokens into a 16-bit paged cache, the
+ * position rotation applied to the keys -- and, in the same launch, to the
+ * tokens' queries when `query` is given.  The call before pa_decode or
+ * pa_decode_mq in a step.
+ *
+ * Tokens.  Row t of key, value, query and query_out is one new token.  With
+ * token_starts (device, [num_seqs + 1] int32, not decreasing) sequence b's
+ * new tokens are the rows token_starts[b] <= t < token_starts[b + 1], none
+ * when the two are equal; rows before token_starts[0] or from
+ * token_starts[num_seqs] on belong to no sequence and are neither read nor
+ * written anywhere.  With token_starts NULL every sequence has num_tokens /
+ * num_seqs of them (num_tokens must be a multiple of num_seqs): row b * q_len
+ * + i.  seq_lens[b] counts the new tokens, as pa_decode expects it
+ * afterwards: the last of them sits at position seq_lens[b] - 1.  A token at
+ * position n goes to row n % block_size of block block_tables[b][n /
+ * block_size].
+ *
+ * Rotation.  cos_sin is [max_positions, rotary_dim] float32: row n holds the
+ * rotary_dim / 2 cosines of position n's angles, then their sines.  With
+ * pairs (i, i + rotary_dim / 2), i < rotary_dim / 2, or (2 i, 2 i + 1) when
+ * interleaved is not 0,
+ *     x'_a = x_a cos_i - x_b sin_i,     x'_b = x_b cos_i + x_a sin_i,
+ * in fp32, rounded once to dtype; dims from rotary_dim on, and values, are
+ * copied.  cos_sin NULL: nothing is rotated.
+ *
+ *   key, value  [num_tokens, num_kv_heads, head_dim] dtype; key_stride and
+ *               value_stride are the elements between tokens (heads and dims
+ *               are contiguous), so that slices of one projection's output
+ *               can be passed as they are
+ *   query, query_out  [num_tokens, num_heads, head_dim] dtype with strides of
+ *               their own, both or neither NULL (num_heads is then ignored);
+ *               query_out may be query with the same stride (in place), and
+ *               must not overlap any other operand
+ *
+ * Supported: head_dim 64, 128 or 256; block_size 8, 16, 32 or 64; rotary_dim
+ * a multiple of 16 up to head_dim.  Operands, caches and cos_sin are 16-byte
+ * aligned and strides multiples of 8 elements, at least the row's length.
+ * num_tokens may be 0.  Device-side problems: PA_STATUS_BAD_SEQ_LEN for a
+ * token at a negative position or past the block table (or token_starts
+ * beyond num_tokens), PA_STATUS_BAD_POSITION for one past cos_sin's rows --
+ * such tokens are not written at all -- and PA_STATUS_BAD_BLOCK_ID, whose
+ * key and value rows are not written.  Two tokens of one call with the same
+ * cache row (sequences that share the block) leave either's values there.
+ */
+PA_API int pa_kv_append(const void *key, const void *value, int64_t key_stride,
+                        int64_t value_stride, const void *query, void *query_out,
+                        int64_t query_stride, int64_t query_out_stride, const float *cos_sin,
+                        int rotary_dim, int max_positions, int interleaved,
+                        const int32_t *block_tables, const int32_t *seq_lens,
+                        const int32_t *token_starts, int num_tokens, int num_seqs, int num_heads,
+                        int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                        int max_blocks_per_seq, int dtype, void *key_cache, void *value_cache,
+                        int32_t *status, pa_stream_t stream);
+
+/*
+ * pa_kv_append into an 8-bit cache; query and query_out stay dtype.  For each
+ * block and KV head that gets new rows, with amax the largest finite
+ * magnitude among them (keys after their rotation, in fp32),
+ *     s = the smallest power of two, 2^-126 at least, with amax <= 448 s,
+ * and, when the block also holds earlier tokens of the sequence, never below
+ * the scale it has: s = max(s, old).  The rows of the earlier tokens are then
+ * re-quantised to a grown scale (code' = e4m3(code * old / s): between powers
+ * of two exact, but for values that fall among e4m3's subnormals).  New codes
+ * are e4m3(x / s), to nearest even; a value that is not finite becomes NaN.
+ * Rows of the block past the sequence's end keep their codes.  A block whose
+ * first row is among the new tokens takes their scale whatever it held.
+ * Sequences must not share a block that either of them appends to: its scale
+ * and rows are then unspecified (nothing else is touched).
+ */
+PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_stride,
+                           int64_t value_stride, const void *query, void *query_out,
+                           int64_t query_stride, int64_t query_out_stride, const float *cos_sin,
+                           int rotary_dim, int max_positions, int interleaved,
+                           const int32_t *block_tables, const int32_t *seq_lens,
+                           const int32_t *token_starts, int num_tokens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                           int max_blocks_per_seq, int dtype, void *key_cache, void *value_cache,
+                           float *k_scales, float *v_scales, int32_t *status, pa_stream_t stream);
+
+/*
+ * Attention over an 8-bit cache: pa_decode (q_len = 1) and pa_decode_mq
+ * (q_len > 1, the same causal rule) with
+ *     K_t = k_scales[block of t][k] * key_cache[...],   V_t likewise.
+ * dtype is the type of query and out; the other arguments are pa_decode_mq's.
+ * Picks V1 or V2 itself, V2 at the partition size pa_decode_q8_partition
+ * returns for (num_seqs, q_len, num_heads, num_kv_heads, head_dim,
+ * max_seq_len_hint if > 0 else max_blocks_per_seq * block_size,
+ * partition_size); after a V2 call the intermediates hold that partitioning's
+ * partials.  They must be valid whenever V2 can be chosen.
+ *
+ * A NaN code in a V row reaches every new token of the KV head's group, those
+ * whose causal limit hides the row included (0 * NaN); NaN in rows past the
+ * sequence's end, or in a K row that a new token does not see, does not.
+ */
+PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *value_cache,
+                        const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                        const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
+                        int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                        int max_blocks_per_seq, int max_seq_len_hint, float scale,
+                        int partition_size, int dtype, void *out, float *tmp_output,
+                        float *exp_sums, float *max_logits, int max_num_partitions,
+                        int32_t *status, pa_stream_t stream);
+
+/*
+ * The partition size pa_decode_q8 runs V2 with for these sizes on the current
+ * device: at least partition_size (intermediates sized for partition_size
+ * always suffice), or 0 when it runs V1.  Negative PA_ERR_* code for invalid
+ * arguments.  Host only.
+ */
+PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                  int head_dim, int max_seq_len, int partition_size);
 
 /*
  * Size of the intermediates array that pa_decode_v2_static keeps inside the

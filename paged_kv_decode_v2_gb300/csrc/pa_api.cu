@@ -9,6 +9,7 @@
 
 #include "pa_decode.h"
 #include "pa_internal.h"
+#include "pa_q8.h"
 
 using namespace pa;
 
@@ -868,6 +869,59 @@ int v1_mq_impl(const void *query, const void *key_cache, const void *value_cache
 }
 
 } // namespace
+
+// The helpers above that the cache operators' entry points share.
+namespace pa {
+
+int host_device(int *dev, int *sms)
+{
+    if (current_device(dev))
+        return PA_ERR_CUDA;
+    *sms = sm_count(*dev);
+    return *sms > 0 ? PA_OK : PA_ERR_CUDA;
+}
+
+int host_check_q_len(int num_seqs, int q_len) { return check_q_len(num_seqs, q_len); }
+
+int host_seq_cap(int max_blocks_per_seq, int block_size, int hint)
+{
+    return seq_cap(max_blocks_per_seq, block_size, hint);
+}
+
+bool host_aligned(const void *p, uintptr_t a) { return aligned(p, a); }
+
+int host_encode_tiled(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base,
+                      const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                      CUtensorMapSwizzle swizzle)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn)
+        return PA_ERR_CUDA;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(map, type, rank, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+void host_tuning(int *warps, int *stages, int *rows_kernel)
+{
+    *warps = g_tune_warps.load(std::memory_order_relaxed);
+    *stages = g_tune_stages.load(std::memory_order_relaxed);
+    *rows_kernel = g_rows_kernel.load(std::memory_order_relaxed);
+}
+
+int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
+               int max_seq_len, int partition_size, int dtype, const float *tmp_output,
+               const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
+               int32_t *status, cudaStream_t stream)
+{
+    return v2_phase2_impl(seq_lens, num_seqs, q_len, num_heads, head_dim, max_seq_len,
+                          partition_size, dtype, tmp_output, exp_sums, max_logits,
+                          max_num_partitions, out, status, stream);
+}
+
+} // namespace pa
 
 extern "C" {
 

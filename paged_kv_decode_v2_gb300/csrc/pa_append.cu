@@ -1,0 +1,604 @@
+// pa_append.cu -- appending the keys and values of new tokens to a paged
+// cache, the position rotation applied on the way, and (optionally) rotating
+// their queries in the same launch.
+//
+// Rotation of a row x at position n, over its first r = rotary_dim dims, by
+// the angles whose cosines c_i and sines s_i the caller tabulates:
+//     x'_a = x_a c_i - x_b s_i,   x'_b = x_b c_i + x_a s_i,   i < r / 2,
+// with (a, b) = (i, i + r / 2), or (2i, 2i + 1) when interleaved; the other
+// dims pass unchanged.  It is computed in fp32 and rounded once, to the
+// storage type (or straight to 8 bits).
+//
+// 16-bit caches: a pure copy with three operations per value, bound by bytes
+// on prompts and by its chain of dependent loads (starts -> length -> block
+// id -> store) on single tokens.  One CTA per token: a thread keeps one pair
+// of 8-dim chunks for the heads it visits, so the token's cosines and sines
+// are read once per thread, and the row loads are issued before anything
+// that depends on the token's place.
+//
+// 8-bit caches (e4m3): the rows of one block and KV head share a scale,
+//     s = the smallest power of two with amax <= 448 s,
+// amax over the block's new rows, and never below the scale the block already
+// has when it holds earlier tokens.  A grown scale re-quantises those rows:
+// between powers of two that only moves exponents (exact, but for values that
+// fall into e4m3's subnormals), so rounding does not build up as a block is
+// filled token by token.  One CTA owns one (block, KV head) -- its rows times
+// pairs of chunks are its threads -- so the maximum is a reduction inside the
+// CTA and no two CTAs write one scale.
+#include <cuda_fp8.h>
+
+#include "pa_device.cuh"
+#include "pa_q8.h"
+
+namespace pa {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendRounds = 4; // rows per thread in flight
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
+{
+    using E = Elem<T>;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = E::lo(w[k]);
+        x[2 * k + 1] = E::hi(w[k]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+{
+    using E = Elem<T>;
+    return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]),
+                      E::pack(x[6], x[7]));
+}
+
+// The sequence of token row t: the number of entries of starts[0 .. n]
+// (non-decreasing) that are <= t, less one; -1 or n when t is in none.  The
+// warp probes 32 entries at a time: one round for up to 32 sequences, two for
+// 1024.
+__device__ __forceinline__ int find_seq(const int32_t *starts, int n, int t, int lane)
+{
+    int lo = 0, hi = n + 1; // the count is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + (lane + 1) * step - 1;
+        const bool le = at < hi && __ldg(starts + at) <= t;
+        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        const int next = min(lo + c * step, hi);
+        hi = min(hi, lo + (c + 1) * step - 1);
+        lo = next;
+        hi = max(hi, lo);
+    }
+    return lo - 1;
+}
+
+// Which two 8-dim chunks of a row item u (of head_dim / 16) covers, and
+// whether it is rotated.  Neighbouring halves: chunk u and the one r / 2 dims
+// up; the dims past rotary_dim, and interleaved rows, chunk by chunk.
+struct Item {
+    int c0, c1;
+    bool rot0, rot1; // interleaved: per chunk; else both or none
+};
+
+__device__ __forceinline__ Item item_of(int u, int rotary_dim, bool interleaved, bool rotate)
+{
+    Item it;
+    const int half = rotary_dim / 16; // chunks of one half
+    if (rotate && !interleaved && u < half) {
+        it.c0 = u;
+        it.c1 = u + half;
+        it.rot0 = it.rot1 = true;
+    } else {
+        it.c0 = 2 * u;
+        it.c1 = 2 * u + 1;
+        it.rot0 = rotate && interleaved && it.c0 * 8 < rotary_dim;
+        it.rot1 = rotate && interleaved && it.c1 * 8 < rotary_dim;
+    }
+    return it;
+}
+
+// The 16 cosines and sines item u needs: neighbouring halves cos[8], sin[8];
+// interleaved 4 cosines and 4 sines for each chunk.
+__device__ __forceinline__ void load_angles(const float *row, const Item &it, int rotary_dim,
+                                            bool interleaved, float (&c)[8], float (&s)[8])
+{
+    const int half = rotary_dim / 2;
+    const int o0 = interleaved ? it.c0 * 4 : it.c0 * 8;
+    const int o1 = interleaved ? it.c1 * 4 : it.c0 * 8 + 4;
+    const bool r1 = interleaved ? it.rot1 : it.rot0;
+    const float4 z = make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 a = it.rot0 ? __ldg(reinterpret_cast<const float4 *>(row + o0)) : z;
+    const float4 b = r1 ? __ldg(reinterpret_cast<const float4 *>(row + o1)) : z;
+    const float4 d = it.rot0 ? __ldg(reinterpret_cast<const float4 *>(row + half + o0)) : z;
+    const float4 e = r1 ? __ldg(reinterpret_cast<const float4 *>(row + half + o1)) : z;
+    c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+    c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
+    s[0] = d.x; s[1] = d.y; s[2] = d.z; s[3] = d.w;
+    s[4] = e.x; s[5] = e.y; s[6] = e.z; s[7] = e.w;
+}
+
+// Products and their difference are rounded one by one (no contraction), as
+// the formula is written.
+__device__ __forceinline__ void rotate_pair(float &a, float &b, float c, float s)
+{
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = x;
+    b = y;
+}
+
+__device__ __forceinline__ void rotate_item(float (&x0)[8], float (&x1)[8], const Item &it,
+                                            bool interleaved, const float (&c)[8],
+                                            const float (&s)[8])
+{
+    if (interleaved) {
+        if (it.rot0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                rotate_pair(x0[2 * k], x0[2 * k + 1], c[k], s[k]);
+        }
+        if (it.rot1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                rotate_pair(x1[2 * k], x1[2 * k + 1], c[4 + k], s[4 + k]);
+        }
+    } else if (it.rot0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            rotate_pair(x0[k], x1[k], c[k], s[k]);
+    }
+}
+
+// Where token row t goes.  Returns false (and sets the status bit) for a row
+// that belongs to no sequence or has no valid position.
+__device__ __forceinline__ bool place_of(const AppendParams &p, int t, int lane, bool reporter,
+                                         int *seq, int *pos)
+{
+    int b, end;
+    if (p.token_starts) {
+        b = find_seq(p.token_starts, p.num_seqs, t, lane);
+        if (b < 0 || b >= p.num_seqs)
+            return false;
+        end = __ldg(p.token_starts + b + 1);
+        if (end > p.num_tokens) {
+            if (reporter)
+                set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+            return false;
+        }
+    } else {
+        b = t / p.q_len;
+        end = (b + 1) * p.q_len;
+    }
+    const int L = __ldg(p.seq_lens + b);
+    const long long at = (long long)L - end + t;
+    if (at < 0 || L > p.max_blocks * p.block_size) {
+        if (reporter)
+            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+        if (at < 0 || at >= (long long)p.max_blocks * p.block_size)
+            return false;
+    }
+    if (p.rotary_dim && at >= p.max_positions) {
+        if (reporter)
+            set_status(p.status, PA_STATUS_BAD_POSITION);
+        return false;
+    }
+    *seq = b;
+    *pos = (int)at;
+    return true;
+}
+
+// One CTA per token row; rows of heads: query, then key, then value.
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int t = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int items = p.head_dim / 16;                 // per row: 4, 8 or 16
+    const int u = threadIdx.x % items;
+    const int row0 = threadIdx.x / items;
+    const int step = kAppendThreads / items;           // rows the CTA covers at once
+    const int rows = p.num_heads + 2 * p.num_kv_heads;
+    const bool interleaved = p.interleaved != 0;
+    const Item rot = item_of(u, p.rotary_dim, interleaved, true);
+    const Item raw = item_of(u, 0, false, false);
+
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) +
+                                                     t * p.query_stride);
+    const uint4 *k = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) +
+                                                     t * p.key_stride);
+    const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) +
+                                                     t * p.value_stride);
+    uint4 *qo = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) + t * p.query_out_stride);
+    const int chunks = p.head_dim / 8;
+
+    int b = 0, pos = 0;
+    bool ok = false, have_place = false;
+    int32_t block = -1;
+    float c[8], s[8];
+    for (int base = row0; base - row0 < rows; base += kAppendRounds * step) {
+        uint4 x0[kAppendRounds], x1[kAppendRounds];
+#pragma unroll
+        for (int i = 0; i < kAppendRounds; ++i) {
+            const int h = base + i * step;
+            if (h < rows) {
+                const bool is_v = h >= p.num_heads + p.num_kv_heads;
+                const Item &it = is_v ? raw : rot;
+                // Plain loads: the query may be rotated in place.
+                const uint4 *src = h < p.num_heads ? q + h * chunks
+                                   : !is_v         ? k + (h - p.num_heads) * chunks
+                                                   : v + (h - p.num_heads - p.num_kv_heads) * chunks;
+                x0[i] = src[it.c0];
+                x1[i] = src[it.c1];
+            }
+        }
+        if (!have_place) {
+            have_place = true;
+            ok = place_of(p, t, lane, threadIdx.x == 0, &b, &pos);
+            if (ok) {
+                block = __ldg(p.block_tables + (size_t)b * p.max_blocks + pos / p.block_size);
+                if (block < 0 || block >= p.num_blocks) {
+                    if (threadIdx.x == 0)
+                        set_status(p.status, PA_STATUS_BAD_BLOCK_ID);
+                    block = -1;
+                }
+                if (p.rotary_dim)
+                    load_angles(p.cos_sin + (size_t)pos * p.rotary_dim, rot, p.rotary_dim,
+                                interleaved, c, s);
+            }
+        }
+        if (!ok)
+            return;
+#pragma unroll
+        for (int i = 0; i < kAppendRounds; ++i) {
+            const int h = base + i * step;
+            if (h >= rows)
+                continue;
+            const bool is_v = h >= p.num_heads + p.num_kv_heads;
+            if (!is_v && (rot.rot0 || rot.rot1)) {
+                float a[8], d[8];
+                unpack8<T>(x0[i], a);
+                unpack8<T>(x1[i], d);
+                rotate_item(a, d, rot, interleaved, c, s);
+                x0[i] = pack8<T>(a);
+                x1[i] = pack8<T>(d);
+            }
+            const Item &it = is_v ? raw : rot;
+            uint4 *dst;
+            if (h < p.num_heads) {
+                dst = qo + h * chunks;
+            } else {
+                if (block < 0)
+                    continue;
+                const int kv = is_v ? h - p.num_heads - p.num_kv_heads : h - p.num_heads;
+                dst = static_cast<uint4 *>(is_v ? p.value_cache : p.key_cache) +
+                      (((size_t)block * p.num_kv_heads + kv) * p.block_size + pos % p.block_size) *
+                          chunks;
+            }
+            dst[it.c0] = x0[i];
+            dst[it.c1] = x1[i];
+        }
+    }
+}
+
+// The smallest power of two s >= 2^-126 with amax <= 448 s (448 = 1.75 * 2^8),
+// from amax's bits.
+__device__ __forceinline__ float scale_of(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+
+// Four values -> four e4m3 codes; a non-finite value becomes e4m3's NaN.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
+{
+    auto clean = [](float x) { return fabsf(x) <= 3.4028234663852886e38f ? x : NAN; };
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(clean(a), clean(b)), __NV_SATFINITE,
+                                                 __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(clean(c), clean(d)), __NV_SATFINITE,
+                                                 __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], float f)
+{
+    return make_uint2(to_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f),
+                      to_e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
+}
+
+__device__ __forceinline__ void from_e4m3x8(uint2 v, float (&x)[8])
+{
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(w[k >> 1] >> ((k & 1) * 16)), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+    }
+}
+
+// Largest finite magnitude.
+__device__ __forceinline__ float amax8(const float (&x)[8], float m)
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float a = fabsf(x[k]);
+        m = a <= 3.4028234663852886e38f ? fmaxf(m, a) : m;
+    }
+    return m;
+}
+
+// Items of the 8-bit append: a sequence's new tokens touch at most n / bs + 2
+// blocks; with token_starts the items of sequence b are numbered from
+// starts[b] / bs + 2 b (strictly increasing, and far enough apart for those
+// blocks: floor(x + n) - floor(x) >= floor(n)), else per sequence alike.
+__host__ __device__ inline int items_per_seq(int q_len, int bs) { return (q_len + bs - 2) / bs + 1; }
+
+// One CTA per (item, KV head), block_size * head_dim / 16 threads: thread =
+// (row of the block, pair of chunks).  CTAs past those rotate one token's
+// query rows each.
+template <typename T>
+__global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, int kv_ctas)
+{
+    __shared__ float s_max[2][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31;
+    const int items = p.head_dim / 16;
+    const int u = threadIdx.x % items;
+    const int row = threadIdx.x / items;
+    const bool interleaved = p.interleaved != 0;
+    const Item rot = item_of(u, p.rotary_dim, interleaved, true);
+    const Item raw = item_of(u, 0, false, false);
+    const int chunks = p.head_dim / 8;
+    float c[8], s[8];
+
+    if ((int)blockIdx.x >= kv_ctas) {
+        // ---- one token's query rows
+        const int t = blockIdx.x - kv_ctas;
+        int b, pos;
+        if (!place_of(p, t, lane, false, &b, &pos))
+            return;
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) +
+                                                         t * p.query_stride);
+        uint4 *qo = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) +
+                                              t * p.query_out_stride);
+        if (p.rotary_dim)
+            load_angles(p.cos_sin + (size_t)pos * p.rotary_dim, rot, p.rotary_dim, interleaved, c, s);
+        const int step = blockDim.x / items;
+        for (int base = row; base < p.num_heads; base += 2 * step) {
+            uint4 x0[2], x1[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (base + i * step < p.num_heads) {
+                    x0[i] = q[(base + i * step) * chunks + rot.c0];
+                    x1[i] = q[(base + i * step) * chunks + rot.c1];
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (base + i * step < p.num_heads) {
+                    float a[8], d[8];
+                    unpack8<T>(x0[i], a);
+                    unpack8<T>(x1[i], d);
+                    rotate_item(a, d, rot, interleaved, c, s);
+                    qo[(base + i * step) * chunks + rot.c0] = pack8<T>(a);
+                    qo[(base + i * step) * chunks + rot.c1] = pack8<T>(d);
+                }
+        }
+        return;
+    }
+
+    // ---- one block of one KV head
+    const int item = blockIdx.x / p.num_kv_heads;
+    const int kv = blockIdx.x % p.num_kv_heads;
+    const int bs = p.block_size;
+    int b, j, begin, end;
+    if (p.token_starts) {
+        // The last sequence whose first item is at or before this one.
+        int lo = 0, hi = p.num_seqs;
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + (lane + 1) * step - 1;
+            const bool le =
+                at < hi && (long long)__ldg(p.token_starts + at) / bs + 2LL * at <= item;
+            const int n = __popc(__ballot_sync(0xffffffffu, le));
+            const int next = min(lo + n * step, hi);
+            hi = max(min(hi, lo + (n + 1) * step - 1), next);
+            lo = next;
+        }
+        b = lo - 1;
+        if (b < 0)
+            return;
+        begin = __ldg(p.token_starts + b);
+        end = __ldg(p.token_starts + b + 1);
+        j = item - (begin / bs + 2 * b);
+    } else {
+        const int per = items_per_seq(p.q_len, bs);
+        b = item / per;
+        j = item % per;
+        begin = b * p.q_len;
+        end = begin + p.q_len;
+    }
+    if (begin >= end || j < 0)
+        return;
+    const bool reporter = threadIdx.x == 0 && kv == 0;
+    if (begin < 0 || end > p.num_tokens) {
+        if (reporter)
+            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+        return;
+    }
+    const int L = __ldg(p.seq_lens + b);
+    const long long first = (long long)L - (end - begin); // position of the first new token
+    const long long cap = (long long)p.max_blocks * bs;
+    if (first < 0 || L > cap) {
+        if (reporter && j == 0)
+            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+    }
+    // Positions written: from `first` (0 when negative) up to L, the table's
+    // and the rotation table's ends.
+    const long long lo_pos = first < 0 ? 0 : first;
+    long long hi_pos = L < cap ? L : cap;
+    if (p.rotary_dim && hi_pos > p.max_positions) {
+        if (reporter && j == 0)
+            set_status(p.status, PA_STATUS_BAD_POSITION);
+        hi_pos = p.max_positions;
+    }
+    const long long blk = lo_pos / bs + j; // logical block
+    const long long p0 = blk * bs;         // its first position
+    if (p0 >= hi_pos)
+        return;
+    const int new_lo = (int)(lo_pos > p0 ? lo_pos - p0 : 0); // rows [new_lo, new_hi) are new
+    const int new_hi = (int)(hi_pos - p0 < bs ? hi_pos - p0 : bs);
+    const int32_t block = __ldg(p.block_tables + (size_t)b * p.max_blocks + blk);
+    if (block < 0 || block >= p.num_blocks) {
+        if (reporter)
+            set_status(p.status, PA_STATUS_BAD_BLOCK_ID);
+        return;
+    }
+    const bool is_new = row >= new_lo && row < new_hi;
+    const size_t slot = (size_t)block * p.num_kv_heads + kv;
+    // Rows below new_lo hold earlier tokens: their scale is a floor.
+    const float old_k = new_lo > 0 ? __ldg(p.k_scales + slot) : 0.f;
+    const float old_v = new_lo > 0 ? __ldg(p.v_scales + slot) : 0.f;
+    float k0[8], k1[8];
+    uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+    float mk = 0.f, mv = 0.f;
+    if (is_new) {
+        const int t = begin + (int)(p0 + row - first);
+        const uint4 *ksrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) +
+                                                            t * p.key_stride) + kv * chunks;
+        const uint4 *vsrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) +
+                                                            t * p.value_stride) + kv * chunks;
+        const uint4 a = ksrc[rot.c0], d = ksrc[rot.c1];
+        v0 = vsrc[raw.c0];
+        v1 = vsrc[raw.c1];
+        if (p.rotary_dim)
+            load_angles(p.cos_sin + (size_t)(p0 + row) * p.rotary_dim, rot, p.rotary_dim,
+                        interleaved, c, s);
+        unpack8<T>(a, k0);
+        unpack8<T>(d, k1);
+        rotate_item(k0, k1, rot, interleaved, c, s);
+        mk = amax8(k1, amax8(k0, 0.f));
+        float x[8];
+        unpack8<T>(v0, x);
+        mv = amax8(x, 0.f);
+        unpack8<T>(v1, x);
+        mv = amax8(x, mv);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+    }
+    if (lane == 0) {
+        s_max[0][threadIdx.x >> 5] = mk;
+        s_max[1][threadIdx.x >> 5] = mv;
+    }
+    __syncthreads();
+    const int warps = blockDim.x >> 5;
+    mk = lane < warps ? s_max[0][lane] : 0.f;
+    mv = lane < warps ? s_max[1][lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+    }
+    const float sk = fmaxf(scale_of(mk), old_k), sv = fmaxf(scale_of(mv), old_v);
+    if (threadIdx.x == 0) {
+        p.k_scales[slot] = sk;
+        p.v_scales[slot] = sv;
+    }
+    uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) +
+                                          (slot * bs + row) * p.head_dim);
+    uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) +
+                                          (slot * bs + row) * p.head_dim);
+    if (is_new) {
+        // x / s is x times an exact power of two for the scales this writes.
+        float x[8];
+        const float fk = 1.f / sk, fv = 1.f / sv;
+        kd[rot.c0] = to_e4m3x8(k0, fk);
+        kd[rot.c1] = to_e4m3x8(k1, fk);
+        unpack8<T>(v0, x);
+        vd[raw.c0] = to_e4m3x8(x, fv);
+        unpack8<T>(v1, x);
+        vd[raw.c1] = to_e4m3x8(x, fv);
+    } else if (row < new_lo) {
+        float x[8];
+        if (sk != old_k) {
+            const float f = old_k / sk;
+            const uint2 a = kd[raw.c0], d = kd[raw.c1];
+            from_e4m3x8(a, x);
+            kd[raw.c0] = to_e4m3x8(x, f);
+            from_e4m3x8(d, x);
+            kd[raw.c1] = to_e4m3x8(x, f);
+        }
+        if (sv != old_v) {
+            const float f = old_v / sv;
+            const uint2 a = vd[raw.c0], d = vd[raw.c1];
+            from_e4m3x8(a, x);
+            vd[raw.c0] = to_e4m3x8(x, f);
+            from_e4m3x8(d, x);
+            vd[raw.c1] = to_e4m3x8(x, f);
+        }
+    }
+}
+
+template <typename F>
+cudaError_t launch_pdl(F *fn, unsigned grid, unsigned threads, cudaStream_t stream, void **args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(fn), args);
+}
+
+} // namespace
+
+cudaError_t launch_append(int dtype, const AppendParams &p, cudaStream_t stream)
+{
+    void *args[] = {const_cast<AppendParams *>(&p)};
+    return dtype == PA_BF16 ? launch_pdl(&append_kernel<__nv_bfloat16>, (unsigned)p.num_tokens,
+                                         kAppendThreads, stream, args)
+                            : launch_pdl(&append_kernel<__half>, (unsigned)p.num_tokens,
+                                         kAppendThreads, stream, args);
+}
+
+static long long append_q8_items(const AppendParams &p)
+{
+    return p.token_starts ? (long long)p.num_tokens / p.block_size + 2LL * p.num_seqs
+                          : (long long)p.num_seqs * items_per_seq(p.q_len, p.block_size);
+}
+
+long long append_q8_ctas(const AppendParams &p)
+{
+    return append_q8_items(p) * p.num_kv_heads + (p.num_heads ? p.num_tokens : 0);
+}
+
+cudaError_t launch_append_q8(int dtype, const AppendParams &p, cudaStream_t stream)
+{
+    int kv_ctas = (int)(append_q8_items(p) * p.num_kv_heads);
+    void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas};
+    const unsigned threads = (unsigned)(p.block_size * p.head_dim / 16);
+    const unsigned grid = (unsigned)append_q8_ctas(p);
+    return dtype == PA_BF16
+               ? launch_pdl(&append_q8_kernel<__nv_bfloat16>, grid, threads, stream, args)
+               : launch_pdl(&append_q8_kernel<__half>, grid, threads, stream, args);
+}
+
+} // namespace pa

@@ -1,0 +1,130 @@
+// pa_q8.h -- host-side interface of the cache operators (appending to a paged
+// cache, attention over an 8-bit cache) between their C entry points
+// (pa_q8_api.cu) and their kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_decode.h"
+#include "pa_internal.h"
+
+namespace pa {
+
+// Host helpers of pa_api.cu that the cache operators share with the 16-bit path.
+int host_device(int *dev, int *sms);             // current device and its SM count
+int host_check_q_len(int num_seqs, int q_len);
+int host_seq_cap(int max_blocks_per_seq, int block_size, int hint);
+bool host_aligned(const void *p, uintptr_t a);
+int host_encode_tiled(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base,
+                      const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                      CUtensorMapSwizzle swizzle);
+void host_tuning(int *warps, int *stages, int *rows_kernel);
+int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
+               int max_seq_len, int partition_size, int dtype, const float *tmp_output,
+               const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
+               int32_t *status, cudaStream_t stream);
+
+// ---------------------------------------------------------------- append
+
+// Arguments of both append kernels.  Token row t belongs to the sequence b
+// with token_starts[b] <= t < token_starts[b + 1] (or b = t / q_len) and sits
+// at position seq_lens[b] - token_starts[b + 1] + t.
+struct AppendParams {
+    const void *key;             // [num_tokens, KV, D], key_stride elements between tokens
+    const void *value;
+    const void *query;           // [num_tokens, H, D] or null
+    void *query_out;
+    long long key_stride, value_stride, query_stride, query_out_stride;
+    const float *cos_sin;        // [max_positions, rotary_dim] (cosines, then sines), or null
+    int rotary_dim;              // 0 without rotation
+    int max_positions;
+    int interleaved;
+    const int32_t *block_tables; // [S, max_blocks]
+    const int32_t *seq_lens;     // [S]
+    const int32_t *token_starts; // [S + 1], or null: q_len tokens per sequence
+    int num_tokens;
+    int num_seqs;
+    int q_len;                   // without token_starts
+    int num_heads;               // 0 without a query
+    int num_kv_heads;
+    int head_dim;
+    int num_blocks;
+    int block_size;
+    int max_blocks;
+    void *key_cache;
+    void *value_cache;
+    float *k_scales;             // 8-bit cache: [num_blocks, KV]
+    float *v_scales;
+    int32_t *status;
+};
+cudaError_t launch_append(int dtype, const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_append_q8(int dtype, const AppendParams &p, cudaStream_t stream);
+// CTAs launch_append_q8 needs (its grid is one-dimensional: at most 2^31 - 1).
+long long append_q8_ctas(const AppendParams &p);
+
+// ---------------------------------------------------------------- attention
+
+// Arguments of the 8-bit attention kernels.
+struct Q8Params {
+    const void *query;           // [S, q_len, H, D], f16 or bf16
+    const float *k_scales;       // [num_blocks, KV]
+    const float *v_scales;
+    const int32_t *block_tables; // [S, max_blocks]
+    const int32_t *seq_lens;     // [S]
+    int dtype;                   // of query and out
+    int num_heads;
+    int num_kv_heads;
+    int group;
+    int q_len;
+    int cols;                    // G * q_len query rows per KV head
+    int col_groups;              // CTAs that split them
+    int num_blocks;
+    int max_blocks;
+    int seq_len_cap;
+    float scale;
+    int partition_size;          // V2
+    int stages;                  // TMA ring stages per warp
+    int max_num_partitions;      // V2: partition capacity of the intermediates
+    float *tmp_output;           // V2
+    float *exp_sums;
+    float *max_logits;
+    void *out;                   // V1
+    int32_t *status;
+};
+
+struct Q8Launch {
+    Q8Params p;
+    CUtensorMap tmap_k;
+    CUtensorMap tmap_v;
+    int head_dim;
+    int block_size;
+    int cta_cols;                // query rows one CTA serves (<= 16)
+    bool v1;
+    dim3 grid;
+    int warps;
+    size_t smem_bytes;
+};
+
+// One ring stage: a K and a V tile of block_size rows (at least 16) of
+// head_dim bytes.
+inline size_t q8_stage_bytes(int block_size, int head_dim)
+{
+    return static_cast<size_t>(block_size < 16 ? 16 : block_size) * head_dim * 2;
+}
+
+// The mma.sync kernels of one head_dim.
+struct Q8Ops {
+    const void *(*kernel)(int block_size, int cta_cols, bool v1);
+};
+const Q8Ops *q8_ops_d64();
+const Q8Ops *q8_ops_d128();
+const Q8Ops *q8_ops_d256();
+
+inline const Q8Ops *q8_ops(int head_dim)
+{
+    return head_dim == 64 ? q8_ops_d64() : head_dim == 128 ? q8_ops_d128() : q8_ops_d256();
+}
+
+} // namespace pa

@@ -1,0 +1,433 @@
+// pa_q8_api.cu -- C entry points of the cache operators declared in
+// include/pa_decode.h: appending to a paged cache (16-bit or 8-bit) and
+// attention over an 8-bit cache.  Host-side validation, TMA descriptors,
+// launch sizing and dispatch.
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "pa_decode.h"
+#include "pa_q8.h"
+
+using namespace pa;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kSlots = 3 * 4 * 2 * 2; // head_dim x block size x n-tiles x V1 / V2
+
+int slot_of(const Q8Launch &L)
+{
+    const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
+    const int bi = L.block_size == 8 ? 0 : L.block_size == 16 ? 1 : L.block_size == 32 ? 2 : 3;
+    return ((di * 4 + bi) * 2 + (L.cta_cols > 8 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0);
+}
+
+const void *kernel_of(const Q8Launch &L)
+{
+    return q8_ops(L.head_dim)->kernel(L.block_size, L.cta_cols, L.v1);
+}
+
+// Per-device, per-kernel dynamic shared memory limit after the opt-in (0 = not yet).
+std::atomic<int> g_limit[kMaxDevices][kSlots];
+// Resident CTAs per SM by [kernel][warps][stages], stored + 1 (0 = not queried).
+std::atomic<int> g_occ[kMaxDevices][kSlots][kMaxWarps + 1][kMaxStages + 1];
+
+size_t smem_limit(int dev, const Q8Launch &L)
+{
+    std::atomic<int> &cell = g_limit[dev][slot_of(L)];
+    const int have = cell.load(std::memory_order_acquire);
+    if (have > 0)
+        return (size_t)have;
+    int optin = 0;
+    cudaFuncAttributes fa;
+    const void *fn = kernel_of(L);
+    if (!fn ||
+        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes)
+        return 0;
+    const int limit = optin - (int)fa.sharedSizeBytes;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
+        return 0;
+    cell.store(limit, std::memory_order_release);
+    return (size_t)limit;
+}
+
+size_t smem_bytes(const Q8Launch &L, int warps, int stages)
+{
+    return 1024 + (size_t)warps * stages * q8_stage_bytes(L.block_size, L.head_dim);
+}
+
+int occupancy(int dev, const Q8Launch &L, int warps, int stages, size_t limit)
+{
+    const size_t smem = smem_bytes(L, warps, stages);
+    if (smem > limit || warps < 1 || warps > kMaxWarps || stages < 1 || stages > kMaxStages)
+        return 0;
+    std::atomic<int> &cell = g_occ[dev][slot_of(L)][warps][stages];
+    const int c = cell.load(std::memory_order_relaxed);
+    if (c)
+        return c - 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel_of(L), warps * 32, smem) !=
+        cudaSuccess)
+        n = 0;
+    cell.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Launch shape: about 64 KB of ring per CTA, three CTAs per SM.
+void size_launch(Q8Launch &L, int dev, int sms, size_t limit)
+{
+    int tune_w, tune_s, rows_kernel;
+    host_tuning(&tune_w, &tune_s, &rows_kernel);
+    auto clampi = [](long long v, int lo, int hi) { return (int)(v < lo ? lo : v > hi ? hi : v); };
+    const size_t sb = q8_stage_bytes(L.block_size, L.head_dim);
+    const size_t scratch = warp_scratch_bytes(L.cta_cols, L.head_dim);
+    const int max_warps = !L.v1 && L.head_dim <= 128 ? 4 : kMaxWarps;
+    int warps = clampi((long long)(65536 / sb), 1, 4);
+    int stages = clampi((long long)(65536 / (warps * sb)), 1, 4);
+    if (L.v1) {
+        warps = clampi((long long)(200 * 1024 / (2 * sb)), 1, kMaxWarps);
+        stages = clampi((long long)(200 * 1024 / (warps * sb)), 1, kMaxStages);
+    }
+    if (tune_s > 0)
+        stages = tune_s;
+    while ((size_t)stages * sb < scratch)
+        ++stages;
+    if (tune_w > 0) {
+        warps = tune_w;
+    } else if (!L.v1) {
+        // A grid of a few waves that fits one wave of narrower CTAs runs those.
+        const long long ctas = (long long)L.grid.x * L.grid.y * L.grid.z;
+        const long long occ = occupancy(dev, L, warps, stages, limit);
+        if (occ > 0 && ctas > occ * sms && ctas <= 3 * occ * sms) {
+            for (int w = warps / 2; w >= 1; w /= 2) {
+                if (ctas <= (long long)occupancy(dev, L, w, stages, limit) * sms) {
+                    warps = w;
+                    break;
+                }
+            }
+        }
+    }
+    warps = warps > max_warps ? max_warps : warps;
+    while (smem_bytes(L, warps, stages) > limit && stages > 1 && (size_t)(stages - 1) * sb >= scratch)
+        --stages;
+    while (smem_bytes(L, warps, stages) > limit && warps > 1)
+        --warps;
+    L.warps = warps;
+    L.p.stages = stages;
+    L.smem_bytes = smem_bytes(L, warps, stages);
+}
+
+// 3-D view of an 8-bit cache for the TMA: dims {row bytes of a slice (64 or
+// 128), slices, rows = num_blocks * KV * block_size}, swizzled by that width,
+// box {slice, 1, block_size}.
+int encode_q8_map(CUtensorMap *map, const void *base, int num_blocks, int num_kv_heads,
+                  int block_size, int head_dim)
+{
+    const uint64_t width = head_dim < 128 ? head_dim : 128;
+    const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * block_size;
+    const uint64_t dims[3] = {width, head_dim / width, rows};
+    const uint64_t strides[2] = {width, (uint64_t)head_dim};
+    const uint32_t box[3] = {(uint32_t)width, 1, (uint32_t)block_size};
+    return host_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box,
+                             width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Shape checks shared by the cache operators.  No CUDA call.
+int check_cache(const void *key_cache, const void *value_cache, const int32_t *block_tables,
+                const int32_t *seq_lens, int num_seqs, int num_kv_heads, int head_dim,
+                int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
+                const int32_t *status)
+{
+    if (!key_cache || !value_cache || !block_tables || !seq_lens)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || block_size <= 0 ||
+        max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (dtype != PA_F16 && dtype != PA_BF16)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return PA_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    // TMA row coordinates and token indices are 32-bit.
+    if ((int64_t)num_blocks * num_kv_heads * block_size > INT32_MAX ||
+        (int64_t)max_blocks_per_seq * block_size > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (!host_aligned(key_cache, 16) || !host_aligned(value_cache, 16) ||
+        !host_aligned(block_tables, 4) || !host_aligned(seq_lens, 4) ||
+        (status && !host_aligned(status, 4)))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+// A strided [num_tokens, heads, head_dim] operand: 16-byte aligned rows that do not overlap.
+bool rows_ok(const void *base, int64_t stride, int heads, int head_dim, int num_tokens)
+{
+    return base && host_aligned(base, 16) && stride % 8 == 0 &&
+           (num_tokens <= 1 || stride >= (int64_t)heads * head_dim);
+}
+
+int append_impl(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                const void *query, void *query_out, int64_t query_stride, int64_t query_out_stride,
+                const float *cos_sin, int rotary_dim, int max_positions, int interleaved,
+                const int32_t *block_tables, const int32_t *seq_lens, const int32_t *token_starts,
+                int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                int num_blocks, int block_size, int max_blocks_per_seq, int dtype, void *key_cache,
+                void *value_cache, float *k_scales, float *v_scales, bool q8, int32_t *status,
+                cudaStream_t stream)
+{
+    int rc = check_cache(key_cache, value_cache, block_tables, seq_lens, num_seqs, num_kv_heads,
+                         head_dim, num_blocks, block_size, max_blocks_per_seq, dtype, status);
+    if (rc)
+        return rc;
+    if (num_tokens < 0 || (query != nullptr) != (query_out != nullptr))
+        return PA_ERR_INVALID_ARG;
+    if (token_starts ? !host_aligned(token_starts, 4) : num_tokens % num_seqs != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!rows_ok(key, key_stride, num_kv_heads, head_dim, num_tokens) ||
+                           !rows_ok(value, value_stride, num_kv_heads, head_dim, num_tokens)))
+        return PA_ERR_INVALID_ARG;
+    if (query && (num_heads <= 0 || num_heads % num_kv_heads != 0))
+        return PA_ERR_INVALID_ARG;
+    if (query && num_tokens > 0 &&
+        (!rows_ok(query, query_stride, num_heads, head_dim, num_tokens) ||
+         !rows_ok(query_out, query_out_stride, num_heads, head_dim, num_tokens)))
+        return PA_ERR_INVALID_ARG;
+    if (q8 && (!k_scales || !v_scales || !host_aligned(k_scales, 4) || !host_aligned(v_scales, 4)))
+        return PA_ERR_INVALID_ARG;
+    if (cos_sin) {
+        if (!host_aligned(cos_sin, 16) || rotary_dim <= 0 || max_positions <= 0)
+            return PA_ERR_INVALID_ARG;
+        if (rotary_dim % 16 != 0 || rotary_dim > head_dim)
+            return PA_ERR_UNSUPPORTED;
+    }
+    if (query && num_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    AppendParams p = {};
+    p.key = key;
+    p.value = value;
+    p.query = query;
+    p.query_out = query_out;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.query_stride = query_stride;
+    p.query_out_stride = query_out_stride;
+    p.cos_sin = cos_sin;
+    p.rotary_dim = cos_sin ? rotary_dim : 0;
+    p.max_positions = max_positions;
+    p.interleaved = interleaved != 0;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.token_starts = token_starts;
+    p.num_tokens = num_tokens;
+    p.num_seqs = num_seqs;
+    p.q_len = token_starts ? 0 : num_tokens / num_seqs;
+    p.num_heads = query ? num_heads : 0;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.max_blocks = max_blocks_per_seq;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.status = status;
+    if (num_tokens == 0)
+        return PA_OK;
+    if (q8 && append_q8_ctas(p) > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    const cudaError_t e = q8 ? launch_append_q8(dtype, p, stream) : launch_append(dtype, p, stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// CTAs that split the query rows of one KV head.
+int row_groups(int cols) { return cols <= 8 ? 1 : (cols + kMaxGroup - 1) / kMaxGroup; }
+
+// The partition size pa_decode_q8 runs V2 with, or 0 for V1.
+int choose_partition(int num_seqs, int q_len, int group, int num_kv_heads, int max_seq_len,
+                     int partition_size, int sms)
+{
+    const int np = pa_v2_num_partitions(max_seq_len, partition_size);
+    const long long v1_ctas = (long long)num_seqs * num_kv_heads * row_groups(q_len * group);
+    if (np <= 1 || (np == 2 && v1_ctas <= sms))
+        return 0;
+    // Twice the partition while the grid still gives every SM its CTAs.
+    long long pc = partition_size;
+    while (pc < 1024 && v1_ctas * pa_v2_num_partitions(max_seq_len, (int)(2 * pc)) >= 6LL * sms)
+        pc *= 2;
+    return pa_v2_num_partitions(max_seq_len, (int)pc) <= 1 ? 0 : (int)pc;
+}
+
+int check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                 int max_seq_len, int partition_size)
+{
+    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+PA_API int pa_kv_append(const void *key, const void *value, int64_t key_stride,
+                        int64_t value_stride, const void *query, void *query_out,
+                        int64_t query_stride, int64_t query_out_stride, const float *cos_sin,
+                        int rotary_dim, int max_positions, int interleaved,
+                        const int32_t *block_tables, const int32_t *seq_lens,
+                        const int32_t *token_starts, int num_tokens, int num_seqs, int num_heads,
+                        int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                        int max_blocks_per_seq, int dtype, void *key_cache, void *value_cache,
+                        int32_t *status, pa_stream_t stream)
+{
+    return append_impl(key, value, key_stride, value_stride, query, query_out, query_stride,
+                       query_out_stride, cos_sin, rotary_dim, max_positions, interleaved,
+                       block_tables, seq_lens, token_starts, num_tokens, num_seqs, num_heads,
+                       num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, dtype,
+                       key_cache, value_cache, nullptr, nullptr, false, status,
+                       (cudaStream_t)stream);
+}
+
+PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_stride,
+                           int64_t value_stride, const void *query, void *query_out,
+                           int64_t query_stride, int64_t query_out_stride, const float *cos_sin,
+                           int rotary_dim, int max_positions, int interleaved,
+                           const int32_t *block_tables, const int32_t *seq_lens,
+                           const int32_t *token_starts, int num_tokens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                           int max_blocks_per_seq, int dtype, void *key_cache, void *value_cache,
+                           float *k_scales, float *v_scales, int32_t *status, pa_stream_t stream)
+{
+    return append_impl(key, value, key_stride, value_stride, query, query_out, query_stride,
+                       query_out_stride, cos_sin, rotary_dim, max_positions, interleaved,
+                       block_tables, seq_lens, token_starts, num_tokens, num_seqs, num_heads,
+                       num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, dtype,
+                       key_cache, value_cache, k_scales, v_scales, true, status,
+                       (cudaStream_t)stream);
+}
+
+PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                  int head_dim, int max_seq_len, int partition_size)
+{
+    if (check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len, partition_size))
+        return -PA_ERR_INVALID_ARG;
+    int dev, sms;
+    if (host_device(&dev, &sms))
+        return -PA_ERR_CUDA;
+    return choose_partition(num_seqs, q_len, num_heads / num_kv_heads, num_kv_heads, max_seq_len,
+                            partition_size, sms);
+}
+
+PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *value_cache,
+                        const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                        const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
+                        int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                        int max_blocks_per_seq, int max_seq_len_hint, float scale,
+                        int partition_size, int dtype, void *out, float *tmp_output,
+                        float *exp_sums, float *max_logits, int max_num_partitions,
+                        int32_t *status, pa_stream_t stream)
+{
+    int rc = check_cache(key_cache, value_cache, block_tables, seq_lens, num_seqs, num_kv_heads,
+                         head_dim, num_blocks, block_size, max_blocks_per_seq, dtype, status);
+    if (rc)
+        return rc;
+    if (!query || !k_scales || !v_scales || !out || num_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || partition_size <= 0 || !std::isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (!host_aligned(query, 4) || !host_aligned(out, 4) || !host_aligned(k_scales, 4) ||
+        !host_aligned(v_scales, 4))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_heads / num_kv_heads;
+    if (group > kMaxGQA || num_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    rc = host_check_q_len(num_seqs, q_len);
+    if (rc)
+        return rc;
+    int dev, sms;
+    if (host_device(&dev, &sms))
+        return PA_ERR_CUDA;
+    const int cap = host_seq_cap(max_blocks_per_seq, block_size, max_seq_len_hint);
+    const int part =
+        choose_partition(num_seqs, q_len, group, num_kv_heads, cap, partition_size, sms);
+    const int np = part ? pa_v2_num_partitions(cap, part) : 1;
+    if (part) {
+        if (!tmp_output || !exp_sums || !max_logits || max_num_partitions <= 0 ||
+            !host_aligned(tmp_output, 16) || !host_aligned(exp_sums, 4) ||
+            !host_aligned(max_logits, 4))
+            return PA_ERR_INVALID_ARG;
+        if (np > max_num_partitions)
+            return PA_ERR_WORKSPACE;
+    }
+
+    Q8Launch L = {};
+    rc = encode_q8_map(&L.tmap_k, key_cache, num_blocks, num_kv_heads, block_size, head_dim);
+    if (rc)
+        return rc;
+    rc = encode_q8_map(&L.tmap_v, value_cache, num_blocks, num_kv_heads, block_size, head_dim);
+    if (rc)
+        return rc;
+    Q8Params &p = L.p;
+    p.query = query;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.dtype = dtype;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.q_len = q_len;
+    p.cols = group * q_len;
+    p.col_groups = row_groups(p.cols);
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.seq_len_cap = cap;
+    p.scale = scale;
+    p.partition_size = part;
+    p.max_num_partitions = max_num_partitions;
+    p.tmp_output = tmp_output;
+    p.exp_sums = exp_sums;
+    p.max_logits = max_logits;
+    p.out = out;
+    p.status = status;
+    L.head_dim = head_dim;
+    L.block_size = block_size;
+    L.cta_cols = p.cols <= 8 ? p.cols : kMaxGroup;
+    L.v1 = part == 0;
+    // Column groups of one partition are adjacent in x: their reads meet in L2.
+    const long long gx = (long long)np * p.col_groups;
+    if (gx > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
+    const size_t limit = smem_limit(dev, L);
+    if (limit == 0)
+        return PA_ERR_CUDA;
+    size_launch(L, dev, sms, limit);
+    if (L.smem_bytes > limit)
+        return PA_ERR_UNSUPPORTED;
+    void *args[] = {&L.tmap_k, &L.tmap_v, &L.p};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = L.grid;
+    cfg.blockDim = dim3(L.warps * 32);
+    cfg.dynamicSmemBytes = L.smem_bytes;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelExC(&cfg, kernel_of(L), args) != cudaSuccess)
+        return PA_ERR_CUDA;
+    if (L.v1)
+        return PA_OK;
+    return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
+                      exp_sums, max_logits, max_num_partitions, out, status, (cudaStream_t)stream);
+}
+
+} // extern "C"

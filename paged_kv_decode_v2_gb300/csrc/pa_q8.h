@@ -81,11 +81,13 @@ struct Q8Params {
     int cols;                    // G * q_len query rows per KV head
     int col_groups;              // CTAs that split them
     int num_blocks;
+    int block_shift;             // log2 of the block size
     int max_blocks;
     int seq_len_cap;
     float scale;
     int partition_size;          // V2
-    int stages;                  // TMA ring stages per warp
+    int stages;                  // TMA ring stages per warp (tcgen05: K ring stages)
+    int v_stages;                // tcgen05: V ring stages
     int max_num_partitions;      // V2: partition capacity of the intermediates
     float *tmp_output;           // V2
     float *exp_sums;
@@ -107,16 +109,16 @@ struct Q8Launch {
     size_t smem_bytes;
 };
 
-// One ring stage: a K and a V tile of block_size rows (at least 16) of
+// One ring stage: a K and a V tile of block_size rows (at least 32) of
 // head_dim bytes.
 inline size_t q8_stage_bytes(int block_size, int head_dim)
 {
-    return static_cast<size_t>(block_size < 16 ? 16 : block_size) * head_dim * 2;
+    return static_cast<size_t>(block_size < 32 ? 32 : block_size) * head_dim * 2;
 }
 
 // The mma.sync kernels of one head_dim.
 struct Q8Ops {
-    const void *(*kernel)(int block_size, int cta_cols, bool v1);
+    const void *(*kernel)(int block_size, int cta_cols, int dtype, bool v1);
 };
 const Q8Ops *q8_ops_d64();
 const Q8Ops *q8_ops_d128();
@@ -125,6 +127,26 @@ const Q8Ops *q8_ops_d256();
 inline const Q8Ops *q8_ops(int head_dim)
 {
     return head_dim == 64 ? q8_ops_d64() : head_dim == 128 ? q8_ops_d128() : q8_ops_d256();
+}
+
+// The tcgen05 kernels: one per (head_dim, rows per CTA), see pa_q8_tc.cuh.
+constexpr int kQ8Tok = 128; // tokens per tile
+struct Q8TcKernel {
+    const void *fn;
+    int threads;
+    int ctas;                // per SM that its registers and tensor memory allow
+    size_t fixed_bytes;      // dynamic shared memory but for the rings
+};
+// rows 8, 16, 32, or (up to head_dim 128) 64; fn null otherwise.
+Q8TcKernel q8_tc_d64(int rows, int dtype, bool v1);
+Q8TcKernel q8_tc_d128(int rows, int dtype, bool v1);
+Q8TcKernel q8_tc_d256(int rows, int dtype, bool v1);
+
+inline Q8TcKernel q8_tc(int head_dim, int rows, int dtype, bool v1)
+{
+    return head_dim == 64    ? q8_tc_d64(rows, dtype, v1)
+           : head_dim == 128 ? q8_tc_d128(rows, dtype, v1)
+                             : q8_tc_d256(rows, dtype, v1);
 }
 
 } // namespace pa

@@ -14,18 +14,19 @@ using namespace pa;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kSlots = 3 * 4 * 2 * 2; // head_dim x block size x n-tiles x V1 / V2
+constexpr int kSlots = 3 * 4 * 2 * 2 * 2; // head_dim x block size x n-tiles x dtype x V1 / V2
 
 int slot_of(const Q8Launch &L)
 {
     const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
     const int bi = L.block_size == 8 ? 0 : L.block_size == 16 ? 1 : L.block_size == 32 ? 2 : 3;
-    return ((di * 4 + bi) * 2 + (L.cta_cols > 8 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0);
+    return (((di * 4 + bi) * 2 + (L.cta_cols > 8 ? 1 : 0)) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 +
+           (L.v1 ? 1 : 0);
 }
 
 const void *kernel_of(const Q8Launch &L)
 {
-    return q8_ops(L.head_dim)->kernel(L.block_size, L.cta_cols, L.v1);
+    return q8_ops(L.head_dim)->kernel(L.block_size, L.cta_cols, L.p.dtype, L.v1);
 }
 
 // Per-device, per-kernel dynamic shared memory limit after the opt-in (0 = not yet).
@@ -73,6 +74,90 @@ int occupancy(int dev, const Q8Launch &L, int warps, int stages, size_t limit)
         n = 0;
     cell.store(n + 1, std::memory_order_relaxed);
     return n;
+}
+
+// ---- tcgen05 kernels
+
+int rows_per_cta(int cols, int head_dim)
+{
+    if (cols <= 8)
+        return 8;
+    if (cols <= 16)
+        return 16;
+    return cols <= 32 || head_dim == 256 ? 32 : 64;
+}
+
+std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
+
+int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
+{
+    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype, L.v1);
+    if (!k.fn)
+        return PA_ERR_UNSUPPORTED;
+    const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
+    const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
+    std::atomic<int> &cell =
+        g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
+    size_t limit = (size_t)cell.load(std::memory_order_acquire);
+    constexpr size_t fixed_static = 8192; // bound of the kernels' static shared memory
+    if (limit == 0) {
+        int optin = 0;
+        cudaFuncAttributes fa;
+        if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+            cudaFuncGetAttributes(&fa, k.fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes ||
+            fa.sharedSizeBytes > fixed_static)
+            return PA_ERR_CUDA;
+        limit = (size_t)optin - fa.sharedSizeBytes;
+        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) != cudaSuccess)
+            return PA_ERR_CUDA;
+        cell.store((int)limit, std::memory_order_release);
+    }
+    const size_t tile = (size_t)kQ8Tok * L.head_dim;
+    int tune_w, tune_s, rows_kernel;
+    host_tuning(&tune_w, &tune_s, &rows_kernel);
+    // As many CTAs per SM as the kernel is made for, if rings of two stages fit.
+    const size_t sm = limit + 1024; // a CTA's 1 KB of system shared memory counts too
+    size_t per_cta = limit;
+    for (int n = k.ctas; n > 1; --n) {
+        if (k.fixed_bytes + 4 * tile + fixed_static <= sm / n - 1024) {
+            per_cta = sm / n - 1024 - fixed_static;
+            break;
+        }
+    }
+    int ks = 1, vs = 1;
+    while (k.fixed_bytes + (ks + vs + 1) * tile <= per_cta && ks + vs < 2 * kMaxStages) {
+        if (ks > vs)
+            ++vs;
+        else
+            ++ks;
+    }
+    if (tune_s > 0)
+        ks = vs = tune_s;
+    if (tune_w > 0)
+        vs = tune_w;
+    while (k.fixed_bytes + (ks + vs) * tile > limit && (ks > 1 || vs > 1)) {
+        if (ks >= vs)
+            --ks;
+        else
+            --vs;
+    }
+    L.smem_bytes = k.fixed_bytes + (ks + vs) * tile;
+    if (L.smem_bytes > limit)
+        return PA_ERR_UNSUPPORTED;
+    L.p.stages = ks;
+    L.p.v_stages = vs;
+    void *args[] = {&L.tmap_k, &L.tmap_v, &L.p};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = L.grid;
+    cfg.blockDim = dim3(k.threads);
+    cfg.dynamicSmemBytes = L.smem_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, k.fn, args) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // Launch shape: about 64 KB of ring per CTA, three CTAs per SM.
@@ -246,14 +331,27 @@ int append_impl(const void *key, const void *value, int64_t key_stride, int64_t 
 }
 
 // CTAs that split the query rows of one KV head.
-int row_groups(int cols) { return cols <= 8 ? 1 : (cols + kMaxGroup - 1) / kMaxGroup; }
+bool use_tc()
+{
+    int w, s, mode;
+    host_tuning(&w, &s, &mode);
+    return mode != 1;
+}
+int row_groups(int cols, int head_dim)
+{
+    if (use_tc()) {
+        const int nr = rows_per_cta(cols, head_dim);
+        return (cols + nr - 1) / nr;
+    }
+    return cols <= 8 ? 1 : (cols + kMaxGroup - 1) / kMaxGroup;
+}
 
 // The partition size pa_decode_q8 runs V2 with, or 0 for V1.
-int choose_partition(int num_seqs, int q_len, int group, int num_kv_heads, int max_seq_len,
-                     int partition_size, int sms)
+int choose_partition(int num_seqs, int q_len, int group, int num_kv_heads, int head_dim,
+                     int max_seq_len, int partition_size, int sms)
 {
     const int np = pa_v2_num_partitions(max_seq_len, partition_size);
-    const long long v1_ctas = (long long)num_seqs * num_kv_heads * row_groups(q_len * group);
+    const long long v1_ctas = (long long)num_seqs * num_kv_heads * row_groups(q_len * group, head_dim);
     if (np <= 1 || (np == 2 && v1_ctas <= sms))
         return 0;
     // Twice the partition while the grid still gives every SM its CTAs.
@@ -320,8 +418,8 @@ PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int nu
     int dev, sms;
     if (host_device(&dev, &sms))
         return -PA_ERR_CUDA;
-    return choose_partition(num_seqs, q_len, num_heads / num_kv_heads, num_kv_heads, max_seq_len,
-                            partition_size, sms);
+    return choose_partition(num_seqs, q_len, num_heads / num_kv_heads, num_kv_heads, head_dim,
+                            max_seq_len, partition_size, sms);
 }
 
 PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *value_cache,
@@ -354,7 +452,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
         return PA_ERR_CUDA;
     const int cap = host_seq_cap(max_blocks_per_seq, block_size, max_seq_len_hint);
     const int part =
-        choose_partition(num_seqs, q_len, group, num_kv_heads, cap, partition_size, sms);
+        choose_partition(num_seqs, q_len, group, num_kv_heads, head_dim, cap, partition_size, sms);
     const int np = part ? pa_v2_num_partitions(cap, part) : 1;
     if (part) {
         if (!tmp_output || !exp_sums || !max_logits || max_num_partitions <= 0 ||
@@ -384,8 +482,9 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.group = group;
     p.q_len = q_len;
     p.cols = group * q_len;
-    p.col_groups = row_groups(p.cols);
+    p.col_groups = row_groups(p.cols, head_dim);
     p.num_blocks = num_blocks;
+    p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
     p.max_blocks = max_blocks_per_seq;
     p.seq_len_cap = cap;
     p.scale = scale;
@@ -405,25 +504,31 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     if (gx > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
-    const size_t limit = smem_limit(dev, L);
-    if (limit == 0)
-        return PA_ERR_CUDA;
-    size_launch(L, dev, sms, limit);
-    if (L.smem_bytes > limit)
-        return PA_ERR_UNSUPPORTED;
-    void *args[] = {&L.tmap_k, &L.tmap_v, &L.p};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = L.grid;
-    cfg.blockDim = dim3(L.warps * 32);
-    cfg.dynamicSmemBytes = L.smem_bytes;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelExC(&cfg, kernel_of(L), args) != cudaSuccess)
-        return PA_ERR_CUDA;
+    if (use_tc()) {
+        rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), (cudaStream_t)stream);
+        if (rc)
+            return rc;
+    } else {
+        const size_t limit = smem_limit(dev, L);
+        if (limit == 0)
+            return PA_ERR_CUDA;
+        size_launch(L, dev, sms, limit);
+        if (L.smem_bytes > limit)
+            return PA_ERR_UNSUPPORTED;
+        void *args[] = {&L.tmap_k, &L.tmap_v, &L.p};
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = L.grid;
+        cfg.blockDim = dim3(L.warps * 32);
+        cfg.dynamicSmemBytes = L.smem_bytes;
+        cfg.stream = (cudaStream_t)stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelExC(&cfg, kernel_of(L), args) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
     if (L.v1)
         return PA_OK;
     return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,

@@ -1,0 +1,976 @@
+// pa_q8_tc.cuh -- attention over a paged cache held in 8 bits (e4m3) with one
+// fp32 scale per (block, KV head) for K and for V, on the tcgen05 tensor
+// cores: phase 1 of split-K decode ("V2") and the single-pass form ("V1"),
+// for one new token or many.
+//
+//     s_t = scale * ks[blk(t)] * <q, kq_t>,    out = sum_t softmax(s)_t vs[blk(t)] vq_t
+//
+// Bound by reading the cache up to about a hundred query rows per KV head, at
+// half the bytes of a 16-bit one.  The codes go into the tensor cores as they
+// are (kind::f8f6f4): nothing is converted, and the arithmetic per cache byte
+// is the query rows' alone.  Tokens are the M side, NR query rows of one KV
+// head the N side, 128 tokens a tile:
+//
+//   S[token, (k, row)]   = K_tile Q_k^T     A = K tile as TMA writes it; B = Q in
+//                          PL e4m3 parts, part k in its own NR columns
+//   P                    = one thread per token: s from its parts' columns,
+//                          scaled by its own block's ks, exponentiated, split
+//                          into three e4m3 parts, written as its row of B
+//   O[dim, (k, row)]    += V_tile^T P_k     A = V tile (M = dims: MN-major),
+//                          B = P (MN-major), part k in its own NR columns
+//
+// Since a thread owns a token, its scales and its mask are its own registers,
+// no reduction crosses lanes in the loop, and l is summed once at the end.
+//
+// Parts.  A value in e4m3 parts is x = x_0 + x_1 / 16 + x_2 / 256, x_k the
+// rounding of 16 times what x_(k-1) left; the parts have accumulators of their
+// own and meet in fp32.  A query row is scaled by the power of two that brings
+// its largest value to [2^7, 2^8): two parts hold bf16's 8 significant bits,
+// three binary16's 11, exactly down to 2^-6 of that (and to 2^-14, 2^-18
+// absolute below).  P, rounded to binary16 first, takes three: off by at most
+// 2^-11 of itself, or 2^-18 where a weight of 1 is 2^4.
+//
+// V's scales go into the softmax's exponent.  With r the largest V scale of the
+// CTA's range and lv_t = log2(vs_t / r), floored at -60,
+//     w_t = 2^(s_t + lv_t - M),   O = sum w_t vq_t,   l = sum w_t 2^(-lv_t),
+// s in log2 units: O / l * r is the output.  M bounds the weighted exponents, so
+// P's rounding is relative to the largest contribution, whatever the blocks'
+// scales.  M moves only when a weight would pass 2^4 (the first tile always);
+// O is rescaled in tensor memory only then.  l and M are a valid pair for the
+// merge: l = sum 2^(s_t - M).
+//
+// Warp roles: warpgroups of softmax warps (16 rows each at most; thread = token
+// = TMEM lane, and dim in the epilogue), one warp that issues the MMAs of S (and
+// owns the tensor memory), one that issues those of P.V, four that issue the TMA loads (half a K or V tile each).
+// S and P have two buffers where tensor memory allows (else one): S of tile
+// t + 2 is issued once the softmax has read S of tile t.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_q8.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+#ifndef Q8_MC
+#define Q8_MC 2
+#endif
+constexpr float kQ8Ln2 = 0.69314718055994531f;
+constexpr float kQ8NoMax = -1e30f; // M before a row has seen a token
+constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4: stored times 2^4, <= 2^8
+constexpr float kQ8Floor = -60.f;  // of log2(vs / r)
+constexpr int kQ8Load = 4;         // producer warps: two for K, two for V
+constexpr int kQ8Chap = 512;       // blocks whose scales are held in shared memory at a time
+
+// ---------------------------------------------------------------- primitives
+
+// Two e4m3 codes (the low half of x) -> two binary16 values.
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t x)
+{
+    uint32_t y;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two binary16 values -> two e4m3 codes in the low half.
+__device__ __forceinline__ uint32_t f16_to_e4m3(uint32_t x)
+{
+    uint32_t y;
+    unsigned short c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(x));
+    y = c;
+    return y;
+}
+
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float fast_log2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Shared-memory matrix descriptor with 128-, 64- or 32-byte swizzle (see
+// smem_desc_sw128; the mode field is 2, 4 or 6, and an atom 8 rows of that width).
+template <int WIDTH>
+__device__ __forceinline__ uint64_t smem_desc_sw(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3fffu);
+    d |= (uint64_t)((lbo >> 4) & 0x3fffu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3fffu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(WIDTH == 128 ? 2 : WIDTH == 64 ? 4 : 6) << 61;
+    return d;
+}
+
+// Instruction descriptor of kind::f8f6f4 with e4m3 operands (formats 0) and an
+// fp32 accumulator; fields as in idesc_f16, bit 15 = A MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool mn_major)
+{
+    return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem], 8-bit operands, K = 32; one thread issues it.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// 8 or 16 consecutive columns of this thread's TMEM lane; valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld(uint32_t ta, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(ta)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t ta, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t ta, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                 "%11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(ta)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+// Waits for this thread's tcgen05.ld; the array is an operand so that no use
+// of its values moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7])::"memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Barrier over `count` threads (a multiple of the warp size), and one that
+// also ORs a predicate over them.
+__device__ __forceinline__ void bar_sync(int id, int count)
+{
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_any(int id, int count, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(count), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
+
+// An int whose order is the float's (no NaN), and back.
+__device__ __forceinline__ int ordered(float x)
+{
+    const int i = __float_as_int(x);
+    return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float unordered(int i)
+{
+    return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
+}
+
+// 2^k and 2^-k for the power of two that brings a row whose largest magnitude
+// is amax to [2^7, 2^8) (k limited to keep both finite).
+__device__ __forceinline__ void q_row_scale(float amax, float &f, float &inv)
+{
+    const int e = (int)(__float_as_uint(amax) >> 23); // biased exponent
+    const int fe = amax > 0.f ? min(127 + 7 - (e - 127), 253) : 127;
+    f = __uint_as_float((uint32_t)fe << 23);
+    inv = __uint_as_float((uint32_t)(254 - fe) << 23);
+}
+
+// ---------------------------------------------------------------- shape
+
+template <int D, int NR, int PL>
+struct Q8Cfg {
+    static constexpr int kRB = D < 128 ? D : 128;                 // bytes of a K/V row in one slice
+    static constexpr int kSlices = D / kRB;
+    static constexpr uint32_t kSlice = kQ8Tok * kRB;              // one slice of a K or V tile
+    static constexpr uint32_t kTile = kQ8Tok * D;
+    static constexpr int kSN = (NR * PL + 15) / 16 * 16;          // columns of S (N of its MMA)
+    static constexpr int kPN = (NR * 3 + 15) / 16 * 16;           // of P, and of O per 128 dims
+    static constexpr int kMB = D == 256 ? 2 : 1;                  // 128-dim halves of O
+    // TMEM columns, in regions of 32: O's halves, then the S buffers.
+    static constexpr int kOReg = (kPN + 31) / 32 * 32;
+    static constexpr int kSReg = (kSN + 31) / 32 * 32;
+    static constexpr int kBuf = kOReg * kMB + 2 * kSReg <= 512 ? 2 : 1; // S and P buffers
+    static constexpr int kNeed = kOReg * kMB + kBuf * kSReg;
+    static constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr uint32_t kSCol = kOReg * kMB;
+    static_assert(kNeed <= 512, "O and S exceed the tensor memory");
+    static constexpr int kPW = kPN <= 32 ? 32 : kPN <= 64 ? 64 : 128; // bytes of P's rows, and
+    static constexpr int kPGroups = (kPN + kPW - 1) / kPW;        // groups of that many columns
+    static constexpr uint32_t kPGroup = kQ8Tok * kPW;
+    static constexpr uint32_t kPBytes = kPGroups * kPGroup;
+    // Where l is summed at the end, [row][token] floats, over P and Q.
+    static constexpr uint32_t kLBytes = NR * kQ8Tok * 4u;
+    static constexpr uint32_t kQBytes = kSN * D;
+    static constexpr int kRW = NR < 16 ? NR : 16;                 // rows of a softmax warpgroup
+    static constexpr int kWG = NR / kRW;
+    static constexpr int kSoft = kWG * 128;
+    static constexpr int kThreads = kSoft + 64 + 32 * kQ8Load;
+    static constexpr int kMinCtas = D > 128 ? 1 : NR <= 8 ? Q8_MC : NR <= 32 ? 2 : 1;
+    static constexpr int kCtas = kMinCtas * (int)kCols <= 512 ? kMinCtas : 512 / (int)kCols;
+    static constexpr uint32_t kPQ = kBuf * kPBytes + kQBytes;
+    static constexpr uint32_t kFixed = 1024 + (kPQ > kLBytes ? kPQ : kLBytes);
+};
+
+template <int D, int NR, int PL, bool V1>
+__global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::kMinCtas)
+    q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
+{
+    using C = Q8Cfg<D, NR, PL>;
+    using T = typename std::conditional<PL == 2, __nv_bfloat16, __half>::type;
+    using E = Elem<T>;
+    constexpr int kRW = C::kRW;
+    constexpr int kMmaWarp = C::kSoft / 32, kTmaWarp = kMmaWarp + 2;
+
+    __shared__ uint64_t k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages],
+        v_empty[kMaxStages];
+    __shared__ uint64_t s_full[2], p_full[2], o_done[2], drained[2];
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    __shared__ __align__(16) float s_cf[NR];   // a row's raw products -> log2 units (but for ks)
+    __shared__ __align__(16) float s_nm[NR];   // kQ8Grow - M
+    __shared__ float s_al[NR];                 // 2^(M_old - M_new)
+    __shared__ float s_inv[NR];                // r / l
+    __shared__ size_t s_row[NR];               // rows of out, or slots of the intermediates
+    __shared__ int s_red[C::kSoft / 32][kRW];
+    __shared__ float s_vref[C::kSoft / 32];
+    __shared__ float s_ks[kQ8Chap], s_vs[kQ8Chap]; // scales of a chapter's blocks
+    extern __shared__ uint8_t dyn_smem[];
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    // blockIdx.x = partition * col_groups + row tile (V1: the row tile).
+    const bool one_group = p.col_groups == 1;
+    const int rt = one_group ? 0 : V1 ? (int)blockIdx.x : (int)blockIdx.x % p.col_groups;
+    const int part = V1 ? 0 : one_group ? (int)blockIdx.x : (int)blockIdx.x / p.col_groups;
+    const int kv = blockIdx.y;
+    const int b = blockIdx.z;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    // Programmatic stream serialisation: nothing global is touched before
+    // the previous grid in the stream has completed.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const int tokA = V1 ? 0 : part * p.partition_size;
+    const int sh = p.block_shift, bs = 1 << sh; // block size
+    const int bpt = kQ8Tok >> sh;               // blocks per tile: 2 to 16
+    const int blk0 = tokA >> sh;
+    const int32_t *bt = p.block_tables + (size_t)b * p.max_blocks + blk0;
+    // The table's first entries, loaded beside the length.
+    int32_t id_first = 0;
+    if (threadIdx.x < C::kSoft && blk0 + (int)threadIdx.x < p.max_blocks)
+        id_first = __ldg(bt + threadIdx.x);
+    int L = __ldg(&p.seq_lens[b]);
+    if (L < 0 || L > p.seq_len_cap) {
+        if (threadIdx.x == 0 && part == 0 && kv == 0 && rt == 0)
+            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+        L = L < 0 ? 0 : p.seq_len_cap;
+    }
+    if (!V1 && tokA >= L)
+        return; // partition past the end of the sequence: nothing to write
+
+    // Rows [c0, c0 + nrows) of the KV head's cols = q_len * group rows.
+    const int c0 = rt * NR;
+    const int nrows = min(NR, p.cols - c0);
+    const int i_last = p.q_len == 1 ? 0 : (c0 + nrows - 1) / p.group;
+    auto row_of = [&](int r) -> size_t { // row of [S * q_len * H] of local row r
+        const int c = c0 + r;
+        if (p.q_len == 1)
+            return (size_t)b * p.num_heads + kv * p.group + c;
+        return ((size_t)b * p.q_len + c / p.group) * p.num_heads + kv * p.group + c % p.group;
+    };
+    // Tokens the CTA needs: [tokA, tokE), the range cut by the causal limit of
+    // its last new token (new token i sees positions <= L - q_len + i).
+    long long e = V1 ? (long long)L : min((long long)L, (long long)tokA + p.partition_size);
+    e = min(e, (long long)L - p.q_len + i_last + 1);
+    const int tokE = (int)e;
+    const int tok0 = blk0 << sh;
+    const int ntiles = tokE > tokA ? (tokE - tok0 + kQ8Tok - 1) / kQ8Tok : 0;
+    const int nblk = tokE > tokA ? (tokE - tok0 + bs - 1) >> sh : 0;
+
+    if (ntiles == 0) {
+        // No row sees a token of the range: an empty partition (m = -inf,
+        // l = 0, o = 0), or a zero output in V1.
+        for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
+            const size_t row = row_of(idx / D);
+            if (V1) {
+                static_cast<T *>(p.out)[row * D + idx % D] = E::from_float(0.f);
+            } else {
+                const size_t slot = row * p.max_num_partitions + part;
+                p.tmp_output[slot * D + idx % D] = 0.f;
+                if (idx % D == 0) {
+                    p.exp_sums[slot] = 0.f;
+                    p.max_logits[slot] = -INFINITY;
+                }
+            }
+        }
+        return;
+    }
+
+    const int kst = p.stages;   // K ring stages
+    const int vst = p.v_stages; // V ring stages
+    const uint32_t smem0 = (smem_addr(dyn_smem) + 1023u) & ~1023u;
+    const uint32_t k_sm = smem0;
+    const uint32_t v_sm = k_sm + (uint32_t)kst * C::kTile;
+    const uint32_t p_sm = v_sm + (uint32_t)vst * C::kTile;
+    const uint32_t q_sm = p_sm + C::kBuf * C::kPBytes;
+    const uint32_t b_k_full = smem_addr(k_full), b_v_full = smem_addr(v_full);
+    const uint32_t b_k_empty = smem_addr(k_empty), b_v_empty = smem_addr(v_empty);
+    const uint32_t b_s_full = smem_addr(s_full), b_p_full = smem_addr(p_full);
+    const uint32_t b_o_done = smem_addr(o_done), b_drained = smem_addr(drained);
+    volatile int *abort_flag = &abort_sh;
+
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&tmem_base_sh), C::kCols);
+        tmem_relinquish();
+    }
+    int32_t status_bits = 0;
+    // Producer warp w loads half w & 1 of the blocks of every K (w < 2) or V tile.
+    // One warp issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80
+    // clocks each) would bound the loop.
+    const int pw = warp - kTmaWarp;
+    const bool is_k = pw < 2;
+    const int p_first = (pw & 1) * (bpt / 2), p_num = bpt / 2; // its blocks of a tile
+    const int p_stages = is_k ? kst : vst;
+    const uint32_t p_full_bar = is_k ? b_k_full : b_v_full, p_empty_bar = is_k ? b_k_empty : b_v_empty;
+    const uint32_t p_ring = is_k ? k_sm : v_sm;
+    const CUtensorMap *p_map = is_k ? &tmap_k : &tmap_v;
+    const uint64_t policy = p.col_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
+    auto fetch_id = [&](int t) -> int32_t { // this lane's block of tile t
+        const int i = t * bpt + p_first + lane;
+        return lane < p_num && i < nblk ? __ldg(bt + i) : 0;
+    };
+    auto load_tile = [&](int s, int t, int32_t id) {
+        const int nb = min(max(nblk - t * bpt - p_first, 0), p_num);
+        if (id < 0 || id >= p.num_blocks) {
+            status_bits |= PA_STATUS_BAD_BLOCK_ID;
+            id = 0; // read a valid block instead of memory outside the cache
+        }
+        const uint32_t bar = p_full_bar + 8 * s;
+        const uint32_t dst = p_ring + (uint32_t)s * C::kTile + p_first * bs * C::kRB;
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, (uint32_t)nb * bs * D);
+        for (int i = 0; i < nb; ++i) {
+            const int32_t phys = __shfl_sync(0xffffffffu, id, i);
+            if (lane == 0) {
+                const int row = (int)(((long long)phys * p.num_kv_heads + kv) * bs);
+#pragma unroll
+                for (int sl = 0; sl < C::kSlices; ++sl)
+                    tma_load_3d(dst + sl * C::kSlice + i * bs * C::kRB, p_map, 0, sl, row, bar, policy);
+            }
+        }
+    };
+    if (threadIdx.x == kTmaWarp * 32) {
+        for (int s = 0; s < kst; ++s) {
+            mbar_init(b_k_full + 8 * s, 2);
+            mbar_init(b_k_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < vst; ++s) {
+            mbar_init(b_v_full + 8 * s, 2);
+            mbar_init(b_v_empty + 8 * s, 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(b_s_full + 8 * j, 1);
+            mbar_init(b_p_full + 8 * j, C::kSoft);
+            mbar_init(b_o_done + 8 * j, 1);
+        }
+        mbar_init(b_drained, 1);
+        mbar_init(b_drained + 8, 1);
+        abort_sh = 0;
+        mbar_init_fence();
+    }
+    int issued = 0;          // tiles this producer has issued
+    int32_t id_next = 0;     // this lane's block of the next one, fetched ahead of its stage
+    if (warp >= kTmaWarp) {
+        // The first tiles, before the rest of the set-up.
+        bar_sync(15, 32 * kQ8Load); // the barriers are initialised
+        id_next = fetch_id(0);
+        while (issued < ntiles && issued < p_stages) {
+            const int32_t id = id_next;
+            id_next = fetch_id(issued + 1);
+            load_tile(issued, issued, id);
+            ++issued;
+        }
+    }
+    // A block's id, or 0 (a valid block) when out of range.
+    auto valid_id = [&](int32_t id) -> int32_t { return id < 0 || id >= p.num_blocks ? 0 : id; };
+
+    float vref = 1.1754943508222875e-38f; // 2^-126, or the range's largest V scale
+    if (warp < kMmaWarp) {
+        // Q rows -> shared memory in PL parts, K-major, swizzled (16-byte chunk c of
+        // row n at c ^ (n & 7), of 64-byte rows c ^ (n >> 1 & 3)); a warp per row.
+        constexpr int kDL = D / 32;                 // consecutive dims of a lane: 2, 4 or 8
+        constexpr int kRows = NR / (C::kSoft / 32); // rows of a warp
+        uint32_t q_raw[kRows][kDL / 2];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = warp + i * (C::kSoft / 32);
+            const uint32_t *q32 = static_cast<const uint32_t *>(p.query) +
+                                  row_of(r < nrows ? r : 0) * (D / 2) + lane * (kDL / 2);
+#pragma unroll
+            for (int k = 0; k < kDL / 2; ++k)
+                q_raw[i][k] = r < nrows ? __ldg(q32 + k) : 0u;
+        }
+        for (int j = threadIdx.x; j < nblk; j += C::kSoft) {
+            const int32_t id = j < C::kSoft ? id_first : __ldg(bt + j);
+            const size_t at = (size_t)valid_id(id) * p.num_kv_heads + kv;
+            const float v = __ldg(p.v_scales + at);
+            vref = fmaxf(vref, v);
+            if (j < kQ8Chap) {
+                s_ks[j] = __ldg(p.k_scales + at);
+                s_vs[j] = v;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = warp + i * (C::kSoft / 32);
+            float x[kDL], m = 0.f;
+#pragma unroll
+            for (int k = 0; k < kDL / 2; ++k) {
+                x[2 * k] = E::lo(q_raw[i][k]);
+                x[2 * k + 1] = E::hi(q_raw[i][k]);
+                m = fmaxf(m, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            float f, inv;
+            q_row_scale(m, f, inv);
+            if (lane == 0) {
+                s_cf[r] = p.scale * inv * kLog2e;
+                s_nm[r] = -kQ8NoMax;
+                const size_t row = row_of(r < nrows ? r : 0);
+                s_row[r] = V1 ? row : row * p.max_num_partitions + part;
+            }
+#pragma unroll
+            for (int k = 0; k < kDL; ++k) // a value that is not finite becomes NaN
+                x[k] = fabsf(x[k]) <= 3.4028234663852886e38f ? x[k] * f : NAN;
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                const int n = k * NR + r;
+                const int d = lane * kDL;          // first dim
+                const int c = (d % C::kRB) >> 4;   // 16-byte chunk
+                const int sw = C::kRB == 128 ? c ^ (n & 7) : c ^ ((n >> 1) & 3);
+                const uint32_t dst = q_sm + (d / C::kRB) * (C::kSN * C::kRB) + n * C::kRB +
+                                     (sw << 4) + (d & 15);
+#pragma unroll
+                for (int h = 0; h < kDL / 2; ++h) {
+                    const uint32_t code = __nv_cvt_float2_to_fp8x2(
+                        make_float2(x[2 * h], x[2 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * h), "h"((unsigned short)code)
+                                 : "memory");
+                    const uint32_t back = e4m3_to_f16(code);
+                    x[2 * h] = (x[2 * h] - Elem<__half>::lo(back)) * 16.f;
+                    x[2 * h + 1] = (x[2 * h + 1] - Elem<__half>::hi(back)) * 16.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
+        if (lane == 0)
+            s_vref[warp] = vref;
+        fence_proxy_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    if (warp >= kTmaWarp) {
+        // ---------------------------------------------------------- producers
+        int s = 0;
+        uint32_t ph = 0u;
+        for (; issued < ntiles; ++issued) {
+            if (!__all_sync(0xffffffffu, mbar_wait_abortable(p_empty_bar + 8 * s, ph, abort_flag))) {
+                status_bits |= PA_STATUS_TIMEOUT;
+                *abort_flag = 1;
+                break;
+            }
+            load_tile(s, issued, id_next);
+            id_next = fetch_id(issued + 1);
+            if (++s == p_stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        // Let copies still in flight land before the shared memory is released
+        // (normally consumed long ago; bounded).
+        for (int t = max(0, issued - p_stages); t < issued; ++t)
+            mbar_wait_bounded(p_full_bar + 8 * (t % p_stages), (uint32_t)(t / p_stages) & 1u, kWaitLimitNs);
+        __syncwarp();
+    } else if (warp >= kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuers
+        // One warp issues the S MMAs, one the P.V MMAs, each as its operands
+        // arrive (an issue takes tens of clocks and a wait a hundred: together
+        // they would bound the loop).  Control flow is warp-uniform and one
+        // elected lane issues, so that descriptors stay in uniform registers.
+        const bool is_s = warp == kMmaWarp;
+        // K-major operands: 8-row groups 8 * kRB bytes apart.
+        const uint64_t qd = smem_desc_sw<C::kRB>(q_sm, 16, 8 * C::kRB);
+        const uint64_t kd = smem_desc_sw<C::kRB>(k_sm, 16, 8 * C::kRB);
+        // MN-major: 8-token groups 8 * row bytes apart, P's column groups a
+        // tile of rows apart.  head_dim 64: M = 128 spans two 64-dim groups; the
+        // second one reads 8 tokens on, into lanes that nothing reads.
+        const uint64_t vd = smem_desc_sw<C::kRB>(v_sm, 8 * C::kRB, 8 * C::kRB);
+        const uint64_t pd = smem_desc_sw<C::kPW>(p_sm, C::kPGroup, 8 * C::kPW);
+        bool ok = true;
+        int s = 0; // ring stage of tile t
+        uint32_t ph = 0u;
+        for (int t = 0; t < ntiles; ++t) {
+            const int j = C::kBuf == 2 ? t & 1 : 0;
+            if (is_s) {
+                // S(t) once K tile t has landed and softmax(t - kBuf) has read the buffer.
+                ok = mbar_wait_abortable(b_k_full + 8 * s, ph, abort_flag) &&
+                     (t < C::kBuf ||
+                      mbar_wait_abortable(b_p_full + 8 * ((t - C::kBuf) & 1),
+                                          (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag));
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint32_t idesc = idesc_e4m3(128, C::kSN, false);
+                    const uint64_t kb = kd + (((uint32_t)s * C::kTile) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        constexpr int kPer = C::kRB / 32;
+                        const uint32_t off_k = (ks / kPer) * C::kSlice + (ks % kPer) * 32;
+                        const uint32_t off_q = (ks / kPer) * (C::kSN * C::kRB) + (ks % kPer) * 32;
+                        tc_mma_f8(tmem + C::kSCol + j * C::kSReg, kb + (off_k >> 4), qd + (off_q >> 4),
+                                  idesc, ks > 0);
+                    }
+                    tc_commit(b_s_full + 8 * (t & 1));
+                    tc_commit(b_k_empty + 8 * s);
+                }
+                __syncwarp();
+                if (++s == kst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            } else {
+                // P.V(t) once P(t) is written and V tile t has landed.
+                ok = mbar_wait_abortable(b_v_full + 8 * s, ph, abort_flag) &&
+                     mbar_wait_abortable(b_p_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint32_t idesc = idesc_e4m3(128, C::kPN, true);
+                    const uint64_t vb = vd + (((uint32_t)s * C::kTile) >> 4);
+                    const uint64_t pb = pd + ((j * C::kPBytes) >> 4);
+#pragma unroll
+                    for (int h = 0; h < C::kMB; ++h)
+#pragma unroll
+                        for (int kt = 0; kt < kQ8Tok / 32; ++kt)
+                            tc_mma_f8(tmem + h * C::kOReg, vb + ((h * C::kSlice + kt * 32 * C::kRB) >> 4),
+                                      pb + ((kt * 32 * C::kPW) >> 4), idesc,
+                                      kt > 0 ? 1u : (t > 0 ? 1u : 0u));
+                    tc_commit(b_o_done + 8 * (t & 1));
+                    tc_commit(b_v_empty + 8 * s);
+                }
+                __syncwarp();
+                if (++s == vst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+            status_bits |= PA_STATUS_TIMEOUT;
+            *abort_flag = 1;
+        }
+        // Every MMA this warp issued has completed once this commit arrives.
+        const uint32_t bar = b_drained + (is_s ? 0 : 8);
+        if (elect_one())
+            tc_commit(bar);
+        __syncwarp();
+        mbar_wait_bounded(bar, 0, kWaitLimitNs);
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        const int wg = warp >> 2;             // rows [wg * kRW, wg * kRW + kRW)
+        const int row0 = wg * kRW;
+        const int tk = threadIdx.x & 127;     // token of the tile, TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+        for (int w = 0; w < C::kSoft / 32; ++w)
+            vref = fmaxf(vref, s_vref[w]);
+        const float vref_lg = fast_log2(vref);
+        // Rows r >= r_min(token) see the token; a tile that every row sees whole
+        // (and that lies inside the range) skips the test.
+        const long long seen_all = min((long long)tokE, (long long)L - p.q_len + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
+        float l_run[kRW];
+#pragma unroll
+        for (int r = 0; r < kRW; ++r)
+            l_run[r] = 0.f;
+        bool ok = true;
+        for (int t = 0; t < ntiles; ++t) {
+            const int j = C::kBuf == 2 ? t & 1 : 0;
+            if (t > 0 && (t * bpt) % kQ8Chap == 0) {
+                // The next chapter of scales (ranges of more than kQ8Chap blocks).
+                bar_sync(1, C::kSoft);
+                for (int i = threadIdx.x; i < kQ8Chap && t * bpt + i < nblk; i += C::kSoft) {
+                    const size_t at = (size_t)valid_id(__ldg(bt + t * bpt + i)) * p.num_kv_heads + kv;
+                    s_ks[i] = __ldg(p.k_scales + at);
+                    s_vs[i] = __ldg(p.v_scales + at);
+                }
+                bar_sync(1, C::kSoft);
+            }
+            const int jb = t * bpt + (tk >> sh); // this token's block of the range
+            const float ks = jb < nblk ? s_ks[jb % kQ8Chap] : 0.f;
+            const float lv = jb < nblk ? fmaxf(fast_log2(s_vs[jb % kQ8Chap]) - vref_lg, kQ8Floor) : 0.f;
+            const float rl = fast_exp2(-lv);
+            const long long first = (long long)tok0 + (long long)t * kQ8Tok, pos = first + tk;
+            const bool full = first >= tokA && first + kQ8Tok <= seen_all;
+            // First visible row of this thread's token: new token i = (c0 + r) /
+            // group sees it when i >= pos - (L - q_len).
+            int r_min = 0;
+            if (!full) {
+                const long long i0 = pos - L + p.q_len;
+                const long long r0 = i0 > 0 ? i0 * p.group - c0 : 0;
+                r_min = pos < tokA || pos >= tokE || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
+            }
+
+            if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (t & 1),
+                                                             (uint32_t)(t >> 1) & 1u, abort_flag)))
+                ok = false;
+            tc_fence_after();
+            const uint32_t sc = lane_base + C::kSCol + (uint32_t)j * C::kSReg + row0;
+            // Exponents of the stored weights, s + lv + (4 - M); with raw, s + lv.
+            float x[kRW];
+            auto exponents = [&](bool raw) -> float {
+                float top = -INFINITY;
+                uint32_t sr[PL][kRW];
+#pragma unroll
+                for (int k = 0; k < PL; ++k)
+                    tmem_ld(sc + k * NR, sr[k]);
+#pragma unroll
+                for (int k = 0; k < PL; ++k)
+                    tmem_wait_ld(sr[k]);
+                const uint64_t ks2 = f2_pack(ks, ks), lv2 = f2_pack(lv, lv);
+#pragma unroll
+                for (int r = 0; r < kRW; r += 4) {
+                    const float4 cf = *reinterpret_cast<const float4 *>(s_cf + row0 + r);
+                    const float4 nm = *reinterpret_cast<const float4 *>(s_nm + row0 + r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = r + 2 * h;
+                        uint64_t s = f2_pack(__uint_as_float(sr[PL - 1][i]),
+                                             __uint_as_float(sr[PL - 1][i + 1]));
+#pragma unroll
+                        for (int k = PL - 2; k >= 0; --k)
+                            s = f2_fma(s, f2_pack(0.0625f, 0.0625f),
+                                       f2_pack(__uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1])));
+                        const uint64_t add =
+                            raw ? lv2 : f2_add(lv2, h ? f2_pack(nm.z, nm.w) : f2_pack(nm.x, nm.y));
+                        f2_unpack(f2_fma(s, f2_mul(ks2, h ? f2_pack(cf.z, cf.w) : f2_pack(cf.x, cf.y)), add),
+                                  x[i], x[i + 1]);
+                    }
+                }
+                if (!full) {
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r)
+                        x[r] = row0 + r >= r_min ? x[r] : -INFINITY;
+                }
+#pragma unroll
+                for (int r = 0; r < kRW; r += 2)
+                    top = fmax3(top, x[r], x[r + 1]);
+                return top;
+            };
+            if (t == 0 || bar_any(2 + wg, 128, exponents(false) > 2.f * kQ8Grow)) {
+                // A weight passes 2^4 in some row: M moves to the rows' maxima over
+                // the tile.
+                exponents(true);
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) {
+                    const int m = __reduce_max_sync(0xffffffffu, ordered(x[r]));
+                    if (lane == 0)
+                        s_red[warp][r] = m;
+                }
+                bar_sync(2 + wg, 128);
+                if (tk < kRW) {
+                    int m = s_red[wg * 4][tk];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w)
+                        m = max(m, s_red[wg * 4 + w][tk]);
+                    const float old = s_nm[row0 + tk];
+                    const float now = fminf(old, kQ8Grow - unordered(m));
+                    s_nm[row0 + tk] = now;
+                    s_al[row0 + tk] = fast_exp2(now - old);
+                }
+                bar_sync(2 + wg, 128);
+                if (t > 0) {
+                    // P.V(t - 1) has to land before O is rescaled (tile 0 has no O yet).
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
+                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                        ok = false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 3 * C::kMB; ++k) {
+                        const uint32_t oc = lane_base + (k / 3) * C::kOReg + (k % 3) * NR + row0;
+#pragma unroll
+                        for (int r8 = 0; r8 < kRW; r8 += 8) {
+                            uint32_t o[8];
+                            tmem_ld(oc + r8, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                o[r] = __float_as_uint(__uint_as_float(o[r]) * s_al[row0 + r8 + r]);
+                            tmem_st(oc + r8, o);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+#pragma unroll
+                for (int r = 0; r < kRW; ++r)
+                    l_run[r] *= s_al[row0 + r];
+                exponents(false);
+            }
+
+            // ---- weights, their sums, and their three parts -> this token's row of P,
+            // once P.V(t - kBuf) has read the buffer
+            if (t >= C::kBuf &&
+                !__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((t - C::kBuf) & 1),
+                                                             (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag)))
+                ok = false;
+            const uint32_t prow = p_sm + (uint32_t)j * C::kPBytes + tk * C::kPW;
+            // 16-byte chunk c of the row, as the swizzle places it.
+            auto chunk = [&](int c) -> uint32_t {
+                constexpr int kLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
+                return (uint32_t)(c ^ ((tk >> kLg) & (C::kPW / 16 - 1))) << 4;
+            };
+            constexpr int kGroup = kRW < 16 ? 8 : 16; // rows whose parts fill one store
+            uint32_t small[3][2];                     // 8 rows: parts of 8 bytes
+#pragma unroll
+            for (int g = 0; g < kRW; g += kGroup) {
+                uint32_t w[3][kGroup / 4];
+#pragma unroll
+                for (int r = 0; r < kGroup; r += 4) {
+                    uint32_t h[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int i = g + r + 2 * q;
+                        const float w0 = fast_exp2(x[i]), w1 = fast_exp2(x[i + 1]);
+                        l_run[i] = fmaf(w0, rl, l_run[i]);
+                        l_run[i + 1] = fmaf(w1, rl, l_run[i + 1]);
+                        h[q] = Elem<__half>::pack(w0, w1);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t a = f16_to_e4m3(h[0]), c = f16_to_e4m3(h[1]);
+                        w[k][r / 4] = __byte_perm(a, c, 0x5410);
+                        if (k < 2) {
+                            // 16 (h - part), exact: 0x4c00 is 16, 0xcc00 -16.
+                            h[0] = h2_fma(e4m3_to_f16(a), 0xcc00cc00u, h2_mul(h[0], 0x4c004c00u));
+                            h[1] = h2_fma(e4m3_to_f16(c), 0xcc00cc00u, h2_mul(h[1], 0x4c004c00u));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    if constexpr (kGroup == 16) {
+                        const int n = k * NR + row0 + g;
+                        const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
+                                     "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
+                                     : "memory");
+                    } else {
+                        small[k][0] = w[k][0];
+                        small[k][1] = w[k][1];
+                    }
+                }
+            }
+            if constexpr (kGroup == 8) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(0)),
+                             "r"(small[0][0]), "r"(small[0][1]), "r"(small[1][0]), "r"(small[1][1])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %3};" ::"r"(prow + chunk(1)),
+                             "r"(small[2][0]), "r"(small[2][1]), "r"(0u)
+                             : "memory");
+            }
+            if (t == ntiles - 1) {
+                // Tile rows past the range (unloaded blocks, slots past the sequence
+                // end) may hold anything: zero them in V so that 0 * NaN cannot reach O.
+                const int vt = tokE - (tok0 + t * kQ8Tok);
+                if (vt < kQ8Tok) {
+                    const int s = t % vst;
+                    // The parity wait is unambiguous once the stage's previous fill has
+                    // landed, which P.V(t - kBuf), done by now, says for a ring of kBuf
+                    // stages or more; a shorter one waits for P.V(t - 1) first.
+                    if (vst < C::kBuf && t > 0 &&
+                        !__all_sync(0xffffffffu,
+                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
+                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                        ok = false;
+                    if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_v_full + 8 * s,
+                                                                     (uint32_t)(t / vst) & 1u, abort_flag)))
+                        ok = false;
+                    const uint32_t vb = v_sm + (uint32_t)s * C::kTile;
+                    constexpr int kChunks = C::kRB / 16;
+                    const int n = (kQ8Tok - vt) * kChunks * C::kSlices;
+                    for (int idx = threadIdx.x; idx < n; idx += C::kSoft) {
+                        const int rest = idx / C::kSlices;
+                        st_shared_zero16(vb + (idx % C::kSlices) * C::kSlice +
+                                         (vt + rest / kChunks) * C::kRB + (rest % kChunks) * 16);
+                    }
+                }
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(b_p_full + 8 * (t & 1));
+        }
+        // P.V(ntiles - 1), the last MMA.
+        if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((ntiles - 1) & 1),
+                                                         (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag)))
+            ok = false;
+        tc_fence_after();
+        if (!ok) {
+            status_bits |= PA_STATUS_TIMEOUT;
+            *abort_flag = 1;
+        }
+
+        // ---- l over the tokens: [row][token] in P's space, then a warp per row
+        float *s_lt = reinterpret_cast<float *>(dyn_smem + (p_sm - smem_addr(dyn_smem)));
+        bar_sync(1, C::kSoft);
+#pragma unroll
+        for (int r = 0; r < kRW; ++r)
+            s_lt[(row0 + r) * 128 + tk] = l_run[r];
+        bar_sync(1, C::kSoft);
+        for (int r = warp; r < NR; r += C::kSoft / 32) {
+            const float4 v = reinterpret_cast<const float4 *>(s_lt + r * 128)[lane];
+            float sum = (v.x + v.y) + (v.z + v.w);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) {
+                s_inv[r] = sum > 0.f ? vref / sum : 0.f; // both O and l hold weights times 2^4
+                if (!V1 && r < nrows && ok) {
+                    p.exp_sums[s_row[r]] = sum * 0.0625f;
+                    p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Grow - s_nm[r]) * kQ8Ln2 : -INFINITY;
+                }
+            }
+        }
+        bar_sync(1, C::kSoft);
+
+        // ---- epilogue: thread = dim, O of its rows from the three parts
+        if (ok && tk < D) {
+#pragma unroll 1
+            for (int h = 0; h < C::kMB; ++h) {
+                const int d = h * 128 + tk;
+#pragma unroll 1
+                for (int r8 = 0; r8 < kRW; r8 += 8) {
+                    uint32_t o[3][8];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_ld(lane_base + h * C::kOReg + k * NR + row0 + r8, o[k]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_wait_ld(o[k]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = row0 + r8 + i;
+                        if (r < nrows) {
+                            const float v = fmaf(fmaf(__uint_as_float(o[2][i]), 0.0625f,
+                                                      __uint_as_float(o[1][i])),
+                                                 0.0625f, __uint_as_float(o[0][i])) * s_inv[r];
+                            if (V1)
+                                static_cast<T *>(p.out)[s_row[r] * D + d] = E::from_float(v);
+                            else
+                                p.tmp_output[s_row[r] * D + d] = v;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    if (status_bits)
+        set_status(p.status, status_bits);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+}
+
+// Kernel and shared memory of one head_dim for NR = 8, 16, 32 or 64 rows (64
+// up to head_dim 128).
+template <int D, int NR>
+static Q8TcKernel q8_tc_pick(int dtype, bool v1)
+{
+    if (dtype == PA_BF16) {
+        using C = Q8Cfg<D, NR, 2>;
+        return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, true>)
+                   : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, false>),
+                C::kThreads, C::kCtas, C::kFixed};
+    }
+    using C = Q8Cfg<D, NR, 3>;
+    return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, true>)
+               : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, false>),
+            C::kThreads, C::kCtas, C::kFixed};
+}
+
+} // namespace pa

@@ -1,0 +1,17 @@
+// Attention over an 8-bit cache on the tcgen05 tensor cores, head_dim 64.
+#include "pa_q8_tc.cuh"
+
+namespace pa {
+
+Q8TcKernel q8_tc_d64(int rows, int dtype, bool v1)
+{
+    switch (rows) {
+    case 8: return q8_tc_pick<64, 8>(dtype, v1);
+    case 16: return q8_tc_pick<64, 16>(dtype, v1);
+    case 32: return q8_tc_pick<64, 32>(dtype, v1);
+    case 64: return q8_tc_pick<64, 64>(dtype, v1);
+    default: return {nullptr, 0, 0, 0};
+    }
+}
+
+} // namespace pa

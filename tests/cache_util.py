@@ -146,7 +146,8 @@ def attend_reference(q, kc, vc, ks, vs, tables, lens, scale):
                 w = qq @ k[:n].T * scale
                 p = torch.softmax(w, dim=1)
                 out[b, i, h * G:(h + 1) * G] = p @ v[:n]
-                off = D * 2.0 ** -23 * (qq.abs() @ k[:n].abs().T).amax(1, keepdim=True) * abs(scale)
+                off = abs(scale) * (D * 2.0 ** -23 * (qq.abs() @ k[:n].abs().T).amax(1, keepdim=True) +
+                                    2.0 ** -17 * qq.abs().amax(1, keepdim=True) * k[:n].abs().sum(1).max())
                 tol[b, i, h * G:(h + 1) * G] = (2.0 ** -11 + 4 * off) * (p @ v[:n].abs()) + \
                     2.0 ** -25 * v[:n].abs().sum(0)
     return out, tol

@@ -98,28 +98,30 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
     const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
     std::atomic<int> &cell =
         g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
-    size_t limit = (size_t)cell.load(std::memory_order_acquire);
-    constexpr size_t fixed_static = 8192; // bound of the kernels' static shared memory
-    if (limit == 0) {
+    // Dynamic limit after the opt-in in the low 18 bits, static bytes above them.
+    int have = cell.load(std::memory_order_acquire);
+    if (have == 0) {
         int optin = 0;
         cudaFuncAttributes fa;
         if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncGetAttributes(&fa, k.fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes ||
-            fa.sharedSizeBytes > fixed_static)
+            cudaFuncGetAttributes(&fa, k.fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes)
             return PA_ERR_CUDA;
-        limit = (size_t)optin - fa.sharedSizeBytes;
-        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) != cudaSuccess)
+        const int dyn = optin - (int)fa.sharedSizeBytes;
+        if (dyn >= 1 << 18 ||
+            cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
             return PA_ERR_CUDA;
-        cell.store((int)limit, std::memory_order_release);
+        have = dyn | (int)fa.sharedSizeBytes << 18;
+        cell.store(have, std::memory_order_release);
     }
+    const size_t limit = have & 0x3ffff, fixed_static = have >> 18;
     const size_t tile = (size_t)kQ8Tok * L.head_dim;
     int tune_w, tune_s, rows_kernel;
     host_tuning(&tune_w, &tune_s, &rows_kernel);
     // As many CTAs per SM as the kernel is made for, if rings of two stages fit.
-    const size_t sm = limit + 1024; // a CTA's 1 KB of system shared memory counts too
+    const size_t sm = limit + fixed_static + 1024; // a CTA also takes 1 KB for the system
     size_t per_cta = limit;
     for (int n = k.ctas; n > 1; --n) {
-        if (k.fixed_bytes + 4 * tile + fixed_static <= sm / n - 1024) {
+        if (k.fixed_bytes + 4 * tile + fixed_static + 1024 <= sm / n) {
             per_cta = sm / n - 1024 - fixed_static;
             break;
         }

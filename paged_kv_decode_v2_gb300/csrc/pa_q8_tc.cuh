@@ -15,20 +15,22 @@
 //                          PL e4m3 parts, part k in its own NR columns
 //   P                    = one thread per token: s from its parts' columns,
 //                          scaled by its own block's ks, exponentiated, split
-//                          into three e4m3 parts, written as its row of B
+//                          into four e5m2 parts, written as its row of B
 //   O[dim, (k, row)]    += V_tile^T P_k     A = V tile (M = dims: MN-major),
 //                          B = P (MN-major), part k in its own NR columns
 //
 // Since a thread owns a token, its scales and its mask are its own registers,
 // no reduction crosses lanes in the loop, and l is summed once at the end.
 //
-// Parts.  A value in e4m3 parts is x = x_0 + x_1 / 16 + x_2 / 256, x_k the
-// rounding of 16 times what x_(k-1) left; the parts have accumulators of their
-// own and meet in fp32.  A query row is scaled by the power of two that brings
-// its largest value to [2^7, 2^8): two parts hold bf16's 8 significant bits,
-// three binary16's 11, exactly down to 2^-6 of that (and to 2^-14, 2^-18
-// absolute below).  P, rounded to binary16 first, takes three: off by at most
-// 2^-11 of itself, or 2^-18 where a weight of 1 is 2^4.
+// Parts.  A query row is scaled by the power of two that brings its largest
+// value to [2^7, 2^8) and held as x = x_0 + x_1 / 16 + x_2 / 256, x_k the e4m3
+// rounding of 16 times what x_(k-1) left: two parts hold bf16's 8 significant
+// bits, three binary16's 11, exactly down to 2^-6 of that scale (and to 2^-14,
+// 2^-18 absolute below); the parts' products meet in fp32.  A weight is rounded
+// to binary16 (2^-12 of itself) and then split without error: e5m2 is binary16's
+// upper byte, so each of the four parts is the upper byte of what the parts
+// before it left (3 + 3 + 3 + 2 bits).  Weights of 1 are stored as 2^11, so that
+// what falls below e5m2's smallest step, 2^-16, is below 2^-27 of them.
 //
 // V's scales go into the softmax's exponent.  With r the largest V scale of the
 // CTA's range and lv_t = log2(vs_t / r), floored at -60,
@@ -61,7 +63,8 @@ namespace pa {
 #endif
 constexpr float kQ8Ln2 = 0.69314718055994531f;
 constexpr float kQ8NoMax = -1e30f; // M before a row has seen a token
-constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4: stored times 2^4, <= 2^8
+constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4,
+constexpr float kQ8Unit = 11.f;    // stored times 2^11: <= 2^15 (e5m2's largest is 1.75 * 2^15)
 constexpr float kQ8Floor = -60.f;  // of log2(vs / r)
 constexpr int kQ8Load = 4;         // producer warps: two for K, two for V
 constexpr int kQ8Chap = 512;       // blocks whose scales are held in shared memory at a time
@@ -76,26 +79,10 @@ __device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t x)
     return y;
 }
 
-// Two binary16 values -> two e4m3 codes in the low half.
-__device__ __forceinline__ uint32_t f16_to_e4m3(uint32_t x)
-{
-    uint32_t y;
-    unsigned short c;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(x));
-    y = c;
-    return y;
-}
-
-__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c)
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -126,11 +113,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw(uint32_t addr, uint32_t lbo, ui
     return d;
 }
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 operands (formats 0) and an
-// fp32 accumulator; fields as in idesc_f16, bit 15 = A MN-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool mn_major)
+// Instruction descriptor of kind::f8f6f4 with an fp32 accumulator, A e4m3
+// (format 0) and B e4m3 or e5m2 (format 1); fields as in idesc_f16, bit 15 = A
+// MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int m, int n, bool b_e5m2, bool mn_major)
 {
-    return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
@@ -241,7 +229,7 @@ struct Q8Cfg {
     static constexpr uint32_t kSlice = kQ8Tok * kRB;              // one slice of a K or V tile
     static constexpr uint32_t kTile = kQ8Tok * D;
     static constexpr int kSN = (NR * PL + 15) / 16 * 16;          // columns of S (N of its MMA)
-    static constexpr int kPN = (NR * 3 + 15) / 16 * 16;           // of P, and of O per 128 dims
+    static constexpr int kPN = NR * 4;                            // of P, and of O per 128 dims
     static constexpr int kMB = D == 256 ? 2 : 1;                  // 128-dim halves of O
     // TMEM columns, in regions of 32: O's halves, then the S buffers.
     static constexpr int kOReg = (kPN + 31) / 32 * 32;
@@ -255,17 +243,15 @@ struct Q8Cfg {
     static constexpr int kPGroups = (kPN + kPW - 1) / kPW;        // groups of that many columns
     static constexpr uint32_t kPGroup = kQ8Tok * kPW;
     static constexpr uint32_t kPBytes = kPGroups * kPGroup;
-    // Where l is summed at the end, [row][token] floats, over P and Q.
-    static constexpr uint32_t kLBytes = NR * kQ8Tok * 4u;
     static constexpr uint32_t kQBytes = kSN * D;
     static constexpr int kRW = NR < 16 ? NR : 16;                 // rows of a softmax warpgroup
     static constexpr int kWG = NR / kRW;
+    static_assert(kWG * 128 <= kQ8Chap, "a thread holds one block of the first chapter");
     static constexpr int kSoft = kWG * 128;
     static constexpr int kThreads = kSoft + 64 + 32 * kQ8Load;
     static constexpr int kMinCtas = D > 128 ? 1 : NR <= 8 ? Q8_MC : NR <= 32 ? 2 : 1;
     static constexpr int kCtas = kMinCtas * (int)kCols <= 512 ? kMinCtas : 512 / (int)kCols;
-    static constexpr uint32_t kPQ = kBuf * kPBytes + kQBytes;
-    static constexpr uint32_t kFixed = 1024 + (kPQ > kLBytes ? kPQ : kLBytes);
+    static constexpr uint32_t kFixed = 1024 + kBuf * kPBytes + kQBytes;
 };
 
 template <int D, int NR, int PL, bool V1>
@@ -285,13 +271,14 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     __shared__ __align__(16) float s_cf[NR];   // a row's raw products -> log2 units (but for ks)
-    __shared__ __align__(16) float s_nm[NR];   // kQ8Grow - M
+    __shared__ __align__(16) float s_nm[NR];   // kQ8Unit - M
     __shared__ float s_al[NR];                 // 2^(M_old - M_new)
     __shared__ float s_inv[NR];                // r / l
     __shared__ size_t s_row[NR];               // rows of out, or slots of the intermediates
     __shared__ int s_red[C::kSoft / 32][kRW];
+    __shared__ float s_part[C::kSoft / 32][kRW];
     __shared__ float s_vref[C::kSoft / 32];
-    __shared__ float s_ks[kQ8Chap], s_vs[kQ8Chap]; // scales of a chapter's blocks
+    __shared__ float s_ks[kQ8Chap], s_lv[kQ8Chap], s_rl[kQ8Chap]; // a chapter's ks, lv, 2^-lv
     extern __shared__ uint8_t dyn_smem[];
 
     const int warp = threadIdx.x >> 5;
@@ -457,6 +444,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     auto valid_id = [&](int32_t id) -> int32_t { return id < 0 || id >= p.num_blocks ? 0 : id; };
 
     float vref = 1.1754943508222875e-38f; // 2^-126, or the range's largest V scale
+    float ks_first = 0.f, vs_first = 0.f; // scales of block threadIdx.x
     if (warp < kMmaWarp) {
         // Q rows -> shared memory in PL parts, K-major, swizzled (16-byte chunk c of
         // row n at c ^ (n & 7), of 64-byte rows c ^ (n >> 1 & 3)); a warp per row.
@@ -472,15 +460,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
             for (int k = 0; k < kDL / 2; ++k)
                 q_raw[i][k] = r < nrows ? __ldg(q32 + k) : 0u;
         }
-        for (int j = threadIdx.x; j < nblk; j += C::kSoft) {
-            const int32_t id = j < C::kSoft ? id_first : __ldg(bt + j);
-            const size_t at = (size_t)valid_id(id) * p.num_kv_heads + kv;
-            const float v = __ldg(p.v_scales + at);
-            vref = fmaxf(vref, v);
-            if (j < kQ8Chap) {
-                s_ks[j] = __ldg(p.k_scales + at);
-                s_vs[j] = v;
-            }
+        if ((int)threadIdx.x < nblk) {
+            const size_t at = (size_t)valid_id(id_first) * p.num_kv_heads + kv;
+            ks_first = __ldg(p.k_scales + at);
+            vs_first = __ldg(p.v_scales + at);
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -526,11 +509,6 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                 }
             }
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
-        if (lane == 0)
-            s_vref[warp] = vref;
         fence_proxy_async();
     }
     tc_fence_before();
@@ -590,7 +568,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    constexpr uint32_t idesc = idesc_e4m3(128, C::kSN, false);
+                    constexpr uint32_t idesc = idesc_f8(128, C::kSN, false, false);
                     const uint64_t kb = kd + (((uint32_t)s * C::kTile) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks) {
@@ -616,7 +594,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    constexpr uint32_t idesc = idesc_e4m3(128, C::kPN, true);
+                    constexpr uint32_t idesc = idesc_f8(128, C::kPN, true, true);
                     const uint64_t vb = vd + (((uint32_t)s * C::kTile) >> 4);
                     const uint64_t pb = pd + ((j * C::kPBytes) >> 4);
 #pragma unroll
@@ -653,43 +631,75 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         const int row0 = wg * kRW;
         const int tk = threadIdx.x & 127;     // token of the tile, TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        // The range's scales (the first S runs meanwhile): the largest V scale of
+        // all, and the first chapter into shared memory.
+        vref = fmaxf(vref, vs_first);
+        for (int j = threadIdx.x + C::kSoft; j < nblk; j += C::kSoft)
+            vref = fmaxf(vref, __ldg(p.v_scales + (size_t)valid_id(__ldg(bt + j)) * p.num_kv_heads + kv));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
+        if (lane == 0)
+            s_vref[warp] = vref;
+        bar_sync(1, C::kSoft);
 #pragma unroll
         for (int w = 0; w < C::kSoft / 32; ++w)
             vref = fmaxf(vref, s_vref[w]);
         const float vref_lg = fast_log2(vref);
+        // Blocks that are not there get ks = 0 and any lv.
+        auto put_scales = [&](int i, float k, float v) {
+            const float lv = fmaxf(fast_log2(v) - vref_lg, kQ8Floor);
+            s_ks[i] = k;
+            s_lv[i] = lv;
+            s_rl[i] = fast_exp2(-lv);
+        };
+        auto load_chapter = [&](int j0, int i0) { // blocks j0 + i, i >= i0
+            for (int i = i0 + threadIdx.x; i < kQ8Chap; i += C::kSoft) {
+                float k = 0.f, v = 0.f;
+                if (j0 + i < nblk) {
+                    const size_t at = (size_t)valid_id(__ldg(bt + j0 + i)) * p.num_kv_heads + kv;
+                    k = __ldg(p.k_scales + at);
+                    v = __ldg(p.v_scales + at);
+                }
+                put_scales(i, k, v);
+                if (j0 + i >= nblk + bpt)
+                    break; // past the last tile
+            }
+        };
+        put_scales(threadIdx.x, ks_first, vs_first);
+        load_chapter(0, C::kSoft);
+        bar_sync(1, C::kSoft);
         // Rows r >= r_min(token) see the token; a tile that every row sees whole
-        // (and that lies inside the range) skips the test.
-        const long long seen_all = min((long long)tokE, (long long)L - p.q_len + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
-        float l_run[kRW];
+        // (and that lies inside the range) skips the test.  Positions from tok0
+        // (a range is less than 2^31 - 128 tokens long: its tiles' ends fit 32 bits).
+        const int rel_a = tokA - tok0, rel_e = tokE - tok0;
+        const int rel_q = L - p.q_len - tok0;
+        const int rel_all = min(rel_e, rel_q + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
+        uint64_t l2[kRW / 2]; // pairs of rows
 #pragma unroll
-        for (int r = 0; r < kRW; ++r)
-            l_run[r] = 0.f;
+        for (int r = 0; r < kRW / 2; ++r)
+            l2[r] = 0;
         bool ok = true;
         for (int t = 0; t < ntiles; ++t) {
             const int j = C::kBuf == 2 ? t & 1 : 0;
             if (t > 0 && (t * bpt) % kQ8Chap == 0) {
                 // The next chapter of scales (ranges of more than kQ8Chap blocks).
                 bar_sync(1, C::kSoft);
-                for (int i = threadIdx.x; i < kQ8Chap && t * bpt + i < nblk; i += C::kSoft) {
-                    const size_t at = (size_t)valid_id(__ldg(bt + t * bpt + i)) * p.num_kv_heads + kv;
-                    s_ks[i] = __ldg(p.k_scales + at);
-                    s_vs[i] = __ldg(p.v_scales + at);
-                }
+                load_chapter(t * bpt, 0);
                 bar_sync(1, C::kSoft);
             }
-            const int jb = t * bpt + (tk >> sh); // this token's block of the range
-            const float ks = jb < nblk ? s_ks[jb % kQ8Chap] : 0.f;
-            const float lv = jb < nblk ? fmaxf(fast_log2(s_vs[jb % kQ8Chap]) - vref_lg, kQ8Floor) : 0.f;
-            const float rl = fast_exp2(-lv);
-            const long long first = (long long)tok0 + (long long)t * kQ8Tok, pos = first + tk;
-            const bool full = first >= tokA && first + kQ8Tok <= seen_all;
+            const int at = (t * bpt + (tk >> sh)) & (kQ8Chap - 1); // this token's block
+            const float ks = s_ks[at], lv = s_lv[at], rl = s_rl[at];
+            const int first = t * kQ8Tok; // from tok0
+            const bool full = first >= rel_a && first + kQ8Tok <= rel_all;
             // First visible row of this thread's token: new token i = (c0 + r) /
             // group sees it when i >= pos - (L - q_len).
             int r_min = 0;
             if (!full) {
-                const long long i0 = pos - L + p.q_len;
-                const long long r0 = i0 > 0 ? i0 * p.group - c0 : 0;
-                r_min = pos < tokA || pos >= tokE || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
+                const int pos = first + tk;
+                const int i0 = pos - rel_q;
+                const long long r0 = i0 > 0 ? (long long)i0 * p.group - c0 : 0;
+                r_min = pos < rel_a || pos >= rel_e || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
             }
 
             if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (t & 1),
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                 ok = false;
             tc_fence_after();
             const uint32_t sc = lane_base + C::kSCol + (uint32_t)j * C::kSReg + row0;
-            // Exponents of the stored weights, s + lv + (4 - M); with raw, s + lv.
+            // Exponents of the stored weights, s + lv + (11 - M); with raw, s + lv.
             float x[kRW];
             auto exponents = [&](bool raw) -> float {
                 float top = -INFINITY;
@@ -738,7 +748,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                     top = fmax3(top, x[r], x[r + 1]);
                 return top;
             };
-            if (t == 0 || bar_any(2 + wg, 128, exponents(false) > 2.f * kQ8Grow)) {
+            if (t == 0 || bar_any(2 + wg, 128, exponents(false) > kQ8Unit + kQ8Grow)) {
                 // A weight passes 2^4 in some row: M moves to the rows' maxima over
                 // the tile.
                 exponents(true);
@@ -755,7 +765,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                     for (int w = 1; w < 4; ++w)
                         m = max(m, s_red[wg * 4 + w][tk]);
                     const float old = s_nm[row0 + tk];
-                    const float now = fminf(old, kQ8Grow - unordered(m));
+                    const float now = fminf(old, kQ8Unit - unordered(m));
                     s_nm[row0 + tk] = now;
                     s_al[row0 + tk] = fast_exp2(now - old);
                 }
@@ -768,8 +778,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                         ok = false;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < 3 * C::kMB; ++k) {
-                        const uint32_t oc = lane_base + (k / 3) * C::kOReg + (k % 3) * NR + row0;
+                    for (int k = 0; k < 4 * C::kMB; ++k) {
+                        const uint32_t oc = lane_base + (k >> 2) * C::kOReg + (k & 3) * NR + row0;
 #pragma unroll
                         for (int r8 = 0; r8 < kRW; r8 += 8) {
                             uint32_t o[8];
@@ -785,11 +795,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                 }
 #pragma unroll
                 for (int r = 0; r < kRW; ++r)
-                    l_run[r] *= s_al[row0 + r];
-                exponents(false);
+                    x[r] += s_nm[row0 + r];
+#pragma unroll
+                for (int r = 0; r < kRW; r += 2)
+                    l2[r / 2] = f2_mul(l2[r / 2], f2_pack(s_al[row0 + r], s_al[row0 + r + 1]));
             }
 
-            // ---- weights, their sums, and their three parts -> this token's row of P,
+            // ---- weights, their sums, and their four parts -> this token's row of P,
             // once P.V(t - kBuf) has read the buffer
             if (t >= C::kBuf &&
                 !__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((t - C::kBuf) & 1),
@@ -801,54 +813,41 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                 constexpr int kLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
                 return (uint32_t)(c ^ ((tk >> kLg) & (C::kPW / 16 - 1))) << 4;
             };
-            constexpr int kGroup = kRW < 16 ? 8 : 16; // rows whose parts fill one store
-            uint32_t small[3][2];                     // 8 rows: parts of 8 bytes
+            uint32_t w[4][kRW / 4]; // part k of rows 4 i .. 4 i + 3
+            const uint64_t rl2 = f2_pack(rl, rl);
 #pragma unroll
-            for (int g = 0; g < kRW; g += kGroup) {
-                uint32_t w[3][kGroup / 4];
+            for (int r = 0; r < kRW; r += 4) {
+                uint32_t h[2];
 #pragma unroll
-                for (int r = 0; r < kGroup; r += 4) {
-                    uint32_t h[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int i = g + r + 2 * q;
-                        const float w0 = fast_exp2(x[i]), w1 = fast_exp2(x[i + 1]);
-                        l_run[i] = fmaf(w0, rl, l_run[i]);
-                        l_run[i + 1] = fmaf(w1, rl, l_run[i + 1]);
-                        h[q] = Elem<__half>::pack(w0, w1);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t a = f16_to_e4m3(h[0]), c = f16_to_e4m3(h[1]);
-                        w[k][r / 4] = __byte_perm(a, c, 0x5410);
-                        if (k < 2) {
-                            // 16 (h - part), exact: 0x4c00 is 16, 0xcc00 -16.
-                            h[0] = h2_fma(e4m3_to_f16(a), 0xcc00cc00u, h2_mul(h[0], 0x4c004c00u));
-                            h[1] = h2_fma(e4m3_to_f16(c), 0xcc00cc00u, h2_mul(h[1], 0x4c004c00u));
-                        }
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    const float w0 = fast_exp2(x[r + 2 * q]), w1 = fast_exp2(x[r + 2 * q + 1]);
+                    l2[r / 2 + q] = f2_fma(f2_pack(w0, w1), rl2, l2[r / 2 + q]);
+                    h[q] = Elem<__half>::pack(w0, w1);
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    if constexpr (kGroup == 16) {
-                        const int n = k * NR + row0 + g;
-                        const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
-                                     "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
-                                     : "memory");
-                    } else {
-                        small[k][0] = w[k][0];
-                        small[k][1] = w[k][1];
+                for (int k = 0; k < 4; ++k) {
+                    w[k][r / 4] = __byte_perm(h[0], h[1], 0x7531); // upper bytes
+                    if (k < 3) {
+                        h[0] = h2_sub(h[0], h[0] & 0xff00ff00u);
+                        h[1] = h2_sub(h[1], h[1] & 0xff00ff00u);
                     }
                 }
             }
-            if constexpr (kGroup == 8) {
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(0)),
-                             "r"(small[0][0]), "r"(small[0][1]), "r"(small[1][0]), "r"(small[1][1])
-                             : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %3};" ::"r"(prow + chunk(1)),
-                             "r"(small[2][0]), "r"(small[2][1]), "r"(0u)
-                             : "memory");
+            if constexpr (kRW == 16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int n = k * NR + row0;
+                    const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
+                                 "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
+                                 : "memory");
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(k / 2)),
+                                 "r"(w[k][0]), "r"(w[k][1]), "r"(w[k + 1][0]), "r"(w[k + 1][1])
+                                 : "memory");
             }
             if (t == ntiles - 1) {
                 // Tile rows past the range (unloaded blocks, slots past the sequence
@@ -881,38 +880,54 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
             tc_fence_before();
             mbar_arrive(b_p_full + 8 * (t & 1));
         }
+        // ---- l over the tokens while the last P.V runs.  In a warp: lanes trade
+        // halves of their rows until each holds one row's sum over a group of
+        // lanes, then those groups meet; warps meet in shared memory.
+        constexpr int kLg = kRW == 16 ? 4 : 3;
+        float l_run[kRW];
+#pragma unroll
+        for (int r = 0; r < kRW; r += 2)
+            f2_unpack(l2[r / 2], l_run[r], l_run[r + 1]);
+#pragma unroll
+        for (int i = 0; i < kLg; ++i) {
+            const int half = kRW >> (i + 1), off = 16 >> i;
+            const bool up = (lane & off) != 0;
+#pragma unroll
+            for (int r = 0; r < half; ++r) {
+                const float give = up ? l_run[r] : l_run[r + half];
+                const float keep = up ? l_run[r + half] : l_run[r];
+                l_run[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        }
+#pragma unroll
+        for (int off = 16 >> kLg; off > 0; off >>= 1)
+            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
+        // Lane bits 4, 3, .. chose the halves: its row is lane >> (5 - kLg).
+        if ((lane & ((32 >> kLg) - 1)) == 0)
+            s_part[warp][lane >> (5 - kLg)] = l_run[0];
+        bar_sync(2 + wg, 128);
+        if (tk < kRW) {
+            float sum = s_part[wg * 4][tk];
+#pragma unroll
+            for (int w = 1; w < 4; ++w)
+                sum += s_part[wg * 4 + w][tk];
+            const int r = row0 + tk;
+            s_inv[r] = sum > 0.f ? vref / sum : 0.f; // O and l hold weights in the same unit
+            if (!V1 && r < nrows) {
+                p.exp_sums[s_row[r]] = sum * 4.8828125e-4f; // 2^-11
+                p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Unit - s_nm[r]) * kQ8Ln2 : -INFINITY;
+            }
+        }
+        bar_sync(2 + wg, 128);
         // P.V(ntiles - 1), the last MMA.
         if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((ntiles - 1) & 1),
-                                                         (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag)))
+                                                    (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag)))
             ok = false;
         tc_fence_after();
         if (!ok) {
             status_bits |= PA_STATUS_TIMEOUT;
             *abort_flag = 1;
         }
-
-        // ---- l over the tokens: [row][token] in P's space, then a warp per row
-        float *s_lt = reinterpret_cast<float *>(dyn_smem + (p_sm - smem_addr(dyn_smem)));
-        bar_sync(1, C::kSoft);
-#pragma unroll
-        for (int r = 0; r < kRW; ++r)
-            s_lt[(row0 + r) * 128 + tk] = l_run[r];
-        bar_sync(1, C::kSoft);
-        for (int r = warp; r < NR; r += C::kSoft / 32) {
-            const float4 v = reinterpret_cast<const float4 *>(s_lt + r * 128)[lane];
-            float sum = (v.x + v.y) + (v.z + v.w);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) {
-                s_inv[r] = sum > 0.f ? vref / sum : 0.f; // both O and l hold weights times 2^4
-                if (!V1 && r < nrows && ok) {
-                    p.exp_sums[s_row[r]] = sum * 0.0625f;
-                    p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Grow - s_nm[r]) * kQ8Ln2 : -INFINITY;
-                }
-            }
-        }
-        bar_sync(1, C::kSoft);
 
         // ---- epilogue: thread = dim, O of its rows from the three parts
         if (ok && tk < D) {
@@ -921,20 +936,20 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
                 const int d = h * 128 + tk;
 #pragma unroll 1
                 for (int r8 = 0; r8 < kRW; r8 += 8) {
-                    uint32_t o[3][8];
+                    uint32_t o[4][8];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
+                    for (int k = 0; k < 4; ++k)
                         tmem_ld(lane_base + h * C::kOReg + k * NR + row0 + r8, o[k]);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
+                    for (int k = 0; k < 4; ++k)
                         tmem_wait_ld(o[k]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = row0 + r8 + i;
                         if (r < nrows) {
-                            const float v = fmaf(fmaf(__uint_as_float(o[2][i]), 0.0625f,
-                                                      __uint_as_float(o[1][i])),
-                                                 0.0625f, __uint_as_float(o[0][i])) * s_inv[r];
+                            const float v = ((__uint_as_float(o[3][i]) + __uint_as_float(o[2][i])) +
+                                             (__uint_as_float(o[1][i]) + __uint_as_float(o[0][i]))) *
+                                            s_inv[r];
                             if (V1)
                                 static_cast<T *>(p.out)[s_row[r] * D + d] = E::from_float(v);
                             else

@@ -911,6 +911,40 @@ void host_tuning(int *warps, int *stages, int *rows_kernel)
     *rows_kernel = g_rows_kernel.load(std::memory_order_relaxed);
 }
 
+bool host_two_tiles(int cols, int head_dim, int cap)
+{
+    return use_tc(cols) && tc_tiles(cols, head_dim, PA_F16, cap) == 2;
+}
+
+int host_mq_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                      int max_seq_len, int partition_size)
+{
+    return pa_decode_mq_partition(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                  partition_size);
+}
+
+int host_mq_over_copy(const void *query, const void *k, const void *v, bool v_half,
+                      const int32_t *flag, const int32_t *offs, const int32_t *table,
+                      const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
+                      int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                      int table_width, int cap, float scale, int part, int np, int dtype, void *out,
+                      float *tmp_output, float *exp_sums, float *max_logits, int32_t *status,
+                      cudaStream_t stream)
+{
+    VhCopy vh{const_cast<void *>(v), const_cast<int32_t *>(flag), offs, num_blocks};
+    const VhCopy *vhp = v_half ? &vh : nullptr;
+    // With V's binary16 copy the bf16 V cache is read only when its flag is set,
+    // and the caller then replaces the result: any valid array will do.
+    const void *v_cache = v_half ? k : v;
+    if (part == 0)
+        return v1_mq_impl(query, k, v_cache, table, seq_lens, num_seqs, q_len, num_heads,
+                          num_kv_heads, head_dim, num_blocks, block_size, table_width, cap, scale,
+                          dtype, out, status, stream, vhp);
+    return v2_mq_impl(query, k, v_cache, table, seq_lens, num_seqs, q_len, num_heads, num_kv_heads,
+                      head_dim, num_blocks, block_size, table_width, cap, scale, part, dtype, out,
+                      tmp_output, exp_sums, max_logits, np, status, stream, vhp);
+}
+
 int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
                int max_seq_len, int partition_size, int dtype, const float *tmp_output,
                const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,

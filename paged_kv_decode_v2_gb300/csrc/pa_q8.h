@@ -26,6 +26,22 @@ int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, 
                const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
                int32_t *status, cudaStream_t stream);
 
+// The 16-bit multi-query attention over copies of K and V (partials at a stride
+// of np partitions of `part` tokens, V1 when part is 0), bf16 with V's binary16
+// copy as pa_decode_mq uses it (v_half; else v is a cache like k).
+int host_mq_over_copy(const void *query, const void *k, const void *v, bool v_half,
+                      const int32_t *flag, const int32_t *offs, const int32_t *table,
+                      const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
+                      int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                      int table_width, int cap, float scale, int part, int np, int dtype, void *out,
+                      float *tmp_output, float *exp_sums, float *max_logits, int32_t *status,
+                      cudaStream_t stream);
+// Whether the two-tile kernel takes binary16 rows of these sizes.
+bool host_two_tiles(int cols, int head_dim, int cap);
+// pa_decode_mq's choice: the partition size of V2, 0 for V1, negative PA_ERR_*.
+int host_mq_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                      int max_seq_len, int partition_size);
+
 // ---------------------------------------------------------------- append
 
 // Arguments of both append kernels.  Token row t belongs to the sequence b
@@ -86,15 +102,34 @@ struct Q8Params {
     int seq_len_cap;
     float scale;
     int partition_size;          // V2
-    int stages;                  // TMA ring stages per warp (tcgen05: K ring stages)
-    int v_stages;                // tcgen05: V ring stages
+    int stages;                  // K ring stages
+    int v_stages;                // V ring stages
     int max_num_partitions;      // V2: partition capacity of the intermediates
     float *tmp_output;           // V2
     float *exp_sums;
     float *max_logits;
     void *out;                   // V1
+    const int32_t *only_if;      // run only if this word is not 0 (null: always)
     int32_t *status;
 };
+
+// The 16-bit copy of a call's blocks (pa_q8_copy.cu).
+struct Q8CopyParams {
+    const void *key_cache, *value_cache;
+    const float *k_scales, *v_scales;
+    const int32_t *block_tables;
+    const int32_t *seq_lens;
+    int num_seqs, num_kv_heads, head_dim, block_size, num_blocks, max_blocks, seq_len_cap;
+    int copy_blocks;             // blocks the copies hold: num_seqs * table_width
+    int table_width;             // of the copies' block table
+    int32_t *offs;               // [num_seqs + 1], the last the total
+    int32_t *flag;
+    int32_t *table;              // [num_seqs, table_width]
+    void *k_copy, *v_copy;
+    int32_t *status;
+};
+cudaError_t launch_q8_copy(int dtype, bool v_half, const Q8CopyParams &p, int num_sms,
+                           cudaStream_t stream);
 
 struct Q8Launch {
     Q8Params p;
@@ -102,32 +137,10 @@ struct Q8Launch {
     CUtensorMap tmap_v;
     int head_dim;
     int block_size;
-    int cta_cols;                // query rows one CTA serves (<= 16)
     bool v1;
     dim3 grid;
-    int warps;
     size_t smem_bytes;
 };
-
-// One ring stage: a K and a V tile of block_size rows (at least 32) of
-// head_dim bytes.
-inline size_t q8_stage_bytes(int block_size, int head_dim)
-{
-    return static_cast<size_t>(block_size < 32 ? 32 : block_size) * head_dim * 2;
-}
-
-// The mma.sync kernels of one head_dim.
-struct Q8Ops {
-    const void *(*kernel)(int block_size, int cta_cols, int dtype, bool v1);
-};
-const Q8Ops *q8_ops_d64();
-const Q8Ops *q8_ops_d128();
-const Q8Ops *q8_ops_d256();
-
-inline const Q8Ops *q8_ops(int head_dim)
-{
-    return head_dim == 64 ? q8_ops_d64() : head_dim == 128 ? q8_ops_d128() : q8_ops_d256();
-}
 
 // The tcgen05 kernels: one per (head_dim, rows per CTA), see pa_q8_tc.cuh.
 constexpr int kQ8Tok = 128; // tokens per tile

@@ -14,68 +14,6 @@ using namespace pa;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kSlots = 3 * 4 * 2 * 2 * 2; // head_dim x block size x n-tiles x dtype x V1 / V2
-
-int slot_of(const Q8Launch &L)
-{
-    const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
-    const int bi = L.block_size == 8 ? 0 : L.block_size == 16 ? 1 : L.block_size == 32 ? 2 : 3;
-    return (((di * 4 + bi) * 2 + (L.cta_cols > 8 ? 1 : 0)) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 +
-           (L.v1 ? 1 : 0);
-}
-
-const void *kernel_of(const Q8Launch &L)
-{
-    return q8_ops(L.head_dim)->kernel(L.block_size, L.cta_cols, L.p.dtype, L.v1);
-}
-
-// Per-device, per-kernel dynamic shared memory limit after the opt-in (0 = not yet).
-std::atomic<int> g_limit[kMaxDevices][kSlots];
-// Resident CTAs per SM by [kernel][warps][stages], stored + 1 (0 = not queried).
-std::atomic<int> g_occ[kMaxDevices][kSlots][kMaxWarps + 1][kMaxStages + 1];
-
-size_t smem_limit(int dev, const Q8Launch &L)
-{
-    std::atomic<int> &cell = g_limit[dev][slot_of(L)];
-    const int have = cell.load(std::memory_order_acquire);
-    if (have > 0)
-        return (size_t)have;
-    int optin = 0;
-    cudaFuncAttributes fa;
-    const void *fn = kernel_of(L);
-    if (!fn ||
-        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncGetAttributes(&fa, fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes)
-        return 0;
-    const int limit = optin - (int)fa.sharedSizeBytes;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess)
-        return 0;
-    cell.store(limit, std::memory_order_release);
-    return (size_t)limit;
-}
-
-size_t smem_bytes(const Q8Launch &L, int warps, int stages)
-{
-    return 1024 + (size_t)warps * stages * q8_stage_bytes(L.block_size, L.head_dim);
-}
-
-int occupancy(int dev, const Q8Launch &L, int warps, int stages, size_t limit)
-{
-    const size_t smem = smem_bytes(L, warps, stages);
-    if (smem > limit || warps < 1 || warps > kMaxWarps || stages < 1 || stages > kMaxStages)
-        return 0;
-    std::atomic<int> &cell = g_occ[dev][slot_of(L)][warps][stages];
-    const int c = cell.load(std::memory_order_relaxed);
-    if (c)
-        return c - 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel_of(L), warps * 32, smem) !=
-        cudaSuccess)
-        n = 0;
-    cell.store(n + 1, std::memory_order_relaxed);
-    return n;
-}
-
 // ---- tcgen05 kernels
 
 int rows_per_cta(int cols, int head_dim)
@@ -160,50 +98,6 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, k.fn, args) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-}
-
-// Launch shape: about 64 KB of ring per CTA, three CTAs per SM.
-void size_launch(Q8Launch &L, int dev, int sms, size_t limit)
-{
-    int tune_w, tune_s, rows_kernel;
-    host_tuning(&tune_w, &tune_s, &rows_kernel);
-    auto clampi = [](long long v, int lo, int hi) { return (int)(v < lo ? lo : v > hi ? hi : v); };
-    const size_t sb = q8_stage_bytes(L.block_size, L.head_dim);
-    const size_t scratch = warp_scratch_bytes(L.cta_cols, L.head_dim);
-    const int max_warps = !L.v1 && L.head_dim <= 128 ? 4 : kMaxWarps;
-    int warps = clampi((long long)(65536 / sb), 1, 4);
-    int stages = clampi((long long)(65536 / (warps * sb)), 1, 4);
-    if (L.v1) {
-        warps = clampi((long long)(200 * 1024 / (2 * sb)), 1, kMaxWarps);
-        stages = clampi((long long)(200 * 1024 / (warps * sb)), 1, kMaxStages);
-    }
-    if (tune_s > 0)
-        stages = tune_s;
-    while ((size_t)stages * sb < scratch)
-        ++stages;
-    if (tune_w > 0) {
-        warps = tune_w;
-    } else if (!L.v1) {
-        // A grid of a few waves that fits one wave of narrower CTAs runs those.
-        const long long ctas = (long long)L.grid.x * L.grid.y * L.grid.z;
-        const long long occ = occupancy(dev, L, warps, stages, limit);
-        if (occ > 0 && ctas > occ * sms && ctas <= 3 * occ * sms) {
-            for (int w = warps / 2; w >= 1; w /= 2) {
-                if (ctas <= (long long)occupancy(dev, L, w, stages, limit) * sms) {
-                    warps = w;
-                    break;
-                }
-            }
-        }
-    }
-    warps = warps > max_warps ? max_warps : warps;
-    while (smem_bytes(L, warps, stages) > limit && stages > 1 && (size_t)(stages - 1) * sb >= scratch)
-        --stages;
-    while (smem_bytes(L, warps, stages) > limit && warps > 1)
-        --warps;
-    L.warps = warps;
-    L.p.stages = stages;
-    L.smem_bytes = smem_bytes(L, warps, stages);
 }
 
 // 3-D view of an 8-bit cache for the TMA: dims {row bytes of a slice (64 or
@@ -333,19 +227,10 @@ int append_impl(const void *key, const void *value, int64_t key_stride, int64_t 
 }
 
 // CTAs that split the query rows of one KV head.
-bool use_tc()
-{
-    int w, s, mode;
-    host_tuning(&w, &s, &mode);
-    return mode != 1;
-}
 int row_groups(int cols, int head_dim)
 {
-    if (use_tc()) {
-        const int nr = rows_per_cta(cols, head_dim);
-        return (cols + nr - 1) / nr;
-    }
-    return cols <= 8 ? 1 : (cols + kMaxGroup - 1) / kMaxGroup;
+    const int nr = rows_per_cta(cols, head_dim);
+    return (cols + nr - 1) / nr;
 }
 
 // The partition size pa_decode_q8 runs V2 with, or 0 for V1.
@@ -361,6 +246,74 @@ int choose_partition(int num_seqs, int q_len, int group, int num_kv_heads, int h
     while (pc < 1024 && v1_ctas * pa_v2_num_partitions(max_seq_len, (int)(2 * pc)) >= 6LL * sms)
         pc *= 2;
     return pa_v2_num_partitions(max_seq_len, (int)pc) <= 1 ? 0 : (int)pc;
+}
+
+// ---- the 16-bit copy for many rows
+
+// From this many query rows per KV head on, the call makes a 16-bit copy of its
+// blocks and runs the 16-bit kernels over it.
+#ifndef Q8CR
+#define Q8CR 256
+#endif
+int copy_rows_default = Q8CR;
+#define kQ8CopyRows copy_rows_default
+
+struct CopyPlan {
+    bool v_half;   // V in binary16 beside a bf16 K, for the two-tile kernel
+    bool may_flag; // some of the copy is binary16
+    int part, np;  // pa_decode_mq's choice
+};
+
+// Lays the copy out in tmp_output behind the partials the 16-bit call writes
+// (256-byte boundaries): the offsets, total and flag, the block table, K, V.
+// False when the worst case's blocks do not fit.
+bool plan_copy(CopyPlan &plan, Q8CopyParams &c, const Q8Params &p, int partition_size, int num_seqs,
+               int block_size, int head_dim)
+{
+    plan.part = host_mq_partition(num_seqs, p.q_len, p.num_heads, p.num_kv_heads, head_dim,
+                                  p.seq_len_cap, partition_size);
+    if (plan.part < 0)
+        return false;
+    plan.np = plan.part ? pa_v2_num_partitions(p.seq_len_cap, plan.part) : 0;
+    if (plan.np > p.max_num_partitions)
+        return false;
+    plan.v_half = p.dtype == PA_BF16 && host_two_tiles(p.cols, head_dim, p.seq_len_cap);
+    plan.may_flag = plan.v_half || p.dtype == PA_F16;
+    const long long width = ((long long)p.seq_len_cap + block_size - 1) / block_size;
+    const long long blocks = width * num_seqs;
+    const long long rows = (long long)p.num_kv_heads * block_size;
+    if (width <= 0 || blocks > INT32_MAX / rows)
+        return false;
+    auto round256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t part_bytes = (size_t)num_seqs * p.q_len * p.num_heads * head_dim * 4;
+    const size_t block_bytes = (size_t)rows * head_dim * 2;
+    const size_t offs = round256(part_bytes * plan.np);
+    const size_t table = offs + round256((size_t)(num_seqs + 2) * 4);
+    const size_t k = table + round256((size_t)blocks * 4);
+    const size_t v = k + round256((size_t)blocks * block_bytes);
+    if (v + (size_t)blocks * block_bytes > part_bytes * p.max_num_partitions)
+        return false;
+    char *base = reinterpret_cast<char *>(p.tmp_output);
+    c.k_scales = p.k_scales;
+    c.v_scales = p.v_scales;
+    c.block_tables = p.block_tables;
+    c.seq_lens = p.seq_lens;
+    c.num_seqs = num_seqs;
+    c.num_kv_heads = p.num_kv_heads;
+    c.head_dim = head_dim;
+    c.block_size = block_size;
+    c.num_blocks = p.num_blocks;
+    c.max_blocks = p.max_blocks;
+    c.seq_len_cap = p.seq_len_cap;
+    c.copy_blocks = (int)blocks;
+    c.table_width = (int)width;
+    c.offs = reinterpret_cast<int32_t *>(base + offs);
+    c.flag = c.offs + num_seqs + 1;
+    c.table = reinterpret_cast<int32_t *>(base + table);
+    c.k_copy = base + k;
+    c.v_copy = base + v;
+    c.status = p.status;
+    return true;
 }
 
 int check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
@@ -452,18 +405,18 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     int dev, sms;
     if (host_device(&dev, &sms))
         return PA_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
     const int cap = host_seq_cap(max_blocks_per_seq, block_size, max_seq_len_hint);
+    const bool work_ok = tmp_output && exp_sums && max_logits && max_num_partitions > 0 &&
+                         host_aligned(tmp_output, 16) && host_aligned(exp_sums, 4) &&
+                         host_aligned(max_logits, 4);
     const int part =
         choose_partition(num_seqs, q_len, group, num_kv_heads, head_dim, cap, partition_size, sms);
     const int np = part ? pa_v2_num_partitions(cap, part) : 1;
-    if (part) {
-        if (!tmp_output || !exp_sums || !max_logits || max_num_partitions <= 0 ||
-            !host_aligned(tmp_output, 16) || !host_aligned(exp_sums, 4) ||
-            !host_aligned(max_logits, 4))
-            return PA_ERR_INVALID_ARG;
-        if (np > max_num_partitions)
-            return PA_ERR_WORKSPACE;
-    }
+    if (part && !work_ok)
+        return PA_ERR_INVALID_ARG;
+    if (part && np > max_num_partitions)
+        return PA_ERR_WORKSPACE;
 
     Q8Launch L = {};
     rc = encode_q8_map(&L.tmap_k, key_cache, num_blocks, num_kv_heads, block_size, head_dim);
@@ -499,42 +452,39 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.status = status;
     L.head_dim = head_dim;
     L.block_size = block_size;
-    L.cta_cols = p.cols <= 8 ? p.cols : kMaxGroup;
     L.v1 = part == 0;
+
+    if (work_ok && p.cols >= kQ8CopyRows) {
+        Q8CopyParams c = {};
+        CopyPlan plan;
+        if (plan_copy(plan, c, p, partition_size, num_seqs, block_size, head_dim)) {
+            c.key_cache = key_cache;
+            c.value_cache = value_cache;
+            if (launch_q8_copy(dtype, plan.v_half, c, sms, st) != cudaSuccess)
+                return PA_ERR_CUDA;
+            rc = host_mq_over_copy(query, c.k_copy, c.v_copy, plan.v_half, c.flag, c.offs, c.table,
+                                   seq_lens, num_seqs, q_len, num_heads, num_kv_heads, head_dim,
+                                   c.copy_blocks, block_size, c.table_width, cap, scale, plan.part,
+                                   plan.np, dtype, out, tmp_output, exp_sums, max_logits, status, st);
+            if (rc || !plan.may_flag)
+                return rc;
+            // Values that binary16 cannot hold: the 8-bit kernel runs after all (V1,
+            // which needs no intermediates, over the result above).
+            p.only_if = c.flag;
+            L.v1 = true;
+            p.partition_size = 0;
+        }
+    }
     // Column groups of one partition are adjacent in x: their reads meet in L2.
-    const long long gx = (long long)np * p.col_groups;
+    const long long gx = (long long)(L.v1 ? 1 : np) * p.col_groups;
     if (gx > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
-    if (use_tc()) {
-        rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), (cudaStream_t)stream);
-        if (rc)
-            return rc;
-    } else {
-        const size_t limit = smem_limit(dev, L);
-        if (limit == 0)
-            return PA_ERR_CUDA;
-        size_launch(L, dev, sms, limit);
-        if (L.smem_bytes > limit)
-            return PA_ERR_UNSUPPORTED;
-        void *args[] = {&L.tmap_k, &L.tmap_v, &L.p};
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = L.grid;
-        cfg.blockDim = dim3(L.warps * 32);
-        cfg.dynamicSmemBytes = L.smem_bytes;
-        cfg.stream = (cudaStream_t)stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelExC(&cfg, kernel_of(L), args) != cudaSuccess)
-            return PA_ERR_CUDA;
-    }
-    if (L.v1)
-        return PA_OK;
+    rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);
+    if (rc || L.v1)
+        return rc;
     return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
-                      exp_sums, max_logits, max_num_partitions, out, status, (cudaStream_t)stream);
+                      exp_sums, max_logits, max_num_partitions, out, status, st);
 }
 
 } // extern "C"

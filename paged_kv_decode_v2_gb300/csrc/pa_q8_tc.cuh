@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     // the previous grid in the stream has completed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (p.only_if && __ldcg(p.only_if) == 0)
+        return;
 
     const int tokA = V1 ? 0 : part * p.partition_size;
     const int sh = p.block_shift, bs = 1 << sh; // block size

@@ -118,7 +118,7 @@ def append_reference(t: Batch, rotated=True):
             yield row, b, pos, block, pos % bs, k, ksize, t.value[row].double(), q, qsize
 
 
-def attend_reference(q, kc, vc, ks, vs, tables, lens, scale):
+def attend_reference(q, kc, vc, ks, vs, tables, lens, scale, held=0.0):
     """(out, tolerance but for the output's own rounding) in 64 bits.  q [S, Q, H, D].
 
     The tolerance: P is rounded to binary16 (2^-11 of each term, doubled for fp32 sums and exp2),
@@ -147,9 +147,10 @@ def attend_reference(q, kc, vc, ks, vs, tables, lens, scale):
                 p = torch.softmax(w, dim=1)
                 out[b, i, h * G:(h + 1) * G] = p @ v[:n]
                 off = abs(scale) * (D * 2.0 ** -23 * (qq.abs() @ k[:n].abs().T).amax(1, keepdim=True) +
+                                    held * (qq.abs() @ k[:n].abs().T).amax(1, keepdim=True) +
                                     2.0 ** -17 * qq.abs().amax(1, keepdim=True) * k[:n].abs().sum(1).max())
-                tol[b, i, h * G:(h + 1) * G] = (2.0 ** -11 + 4 * off) * (p @ v[:n].abs()) + \
-                    2.0 ** -25 * v[:n].abs().sum(0)
+                tol[b, i, h * G:(h + 1) * G] = (2.0 ** -11 + held + 4 * off) * (p @ v[:n].abs()) + \
+                    2.0 ** -25 * v[:n].abs().sum(0) + 448 * 2.0 ** -60 * float(vs[ids, h].max())
     return out, tol
 
 

@@ -79,14 +79,14 @@ def run(pa, q, cache, scale, P, hint=0):
     return out.view(S, Q, H, D).cpu(), int(status.item())
 
 
-def check(pa, lens, Q=1, G=4, KV=2, D=64, bs=16, P=64, dtype=BF16, scale=None, seed=0, q=None, hint=0, **cache):
+def check(pa, lens, Q=1, G=4, KV=2, D=64, bs=16, P=64, dtype=BF16, scale=None, seed=0, q=None, hint=0, held=0.0, **cache):
     c = cu.cache8(lens, KV=KV, D=D, bs=bs, seed=seed, **cache)
     g = torch.Generator().manual_seed(seed + 1)
     if q is None:
         q = torch.randn((len(lens), Q, G * KV, D), generator=g).to(dtype)
     scale = 1 / math.sqrt(D) if scale is None else scale
     out, status = run(pa, q, c, scale, P, hint)
-    ref, tol = cu.attend_reference(q, c[0], c[1], *[torch.nan_to_num(x) for x in c[2:4]], *c[4:], scale)
+    ref, tol = cu.attend_reference(q, c[0], c[1], *[torch.nan_to_num(x) for x in c[2:4]], *c[4:], scale, held)
     assert status == 0
     tol = tol + cu.rounding(ref.abs() + tol, dtype)
     # binary16's largest value is 65504 and its next step would be 65536: results from the middle,
@@ -134,6 +134,20 @@ def test_scales(pa, scales, bs, Q, G):
 def test_poisoned_slots_are_not_read(pa, D, bs, Q, G):
     check(pa, [20, 1, 77, 129], Q=Q, G=G, D=D, bs=bs, poison=True)
     check(pa, [20, 1, 77, 129], Q=Q, G=G, D=D, bs=bs, poison=True, P=512)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,bs,KV", [(64, 16, 2), (128, 16, 2), (128, 64, 1), (256, 32, 1), (64, 8, 3)])
+def test_many_rows(pa, D, bs, KV, dtype):
+    """Hundreds of rows per KV head, where the call may work on a 16-bit copy: short and long
+    sequences, stale NaN rows, scales that are no powers of two, and values no copy can hold."""
+    many = dict(Q=90, G=4, D=D, bs=bs, KV=KV, dtype=dtype, P=128)
+    check(pa, [1100, 90, 300, 0, 33], poison=True, **many)
+    check(pa, [200, 131], poison=True, **many)
+    check(pa, [1100, 95], scales="any", held=cu.HALF_STEP[dtype], **many)
+    check(pa, [1100, 95], scales="wild", **many)
+    check(pa, [1100, 95], scales="zero", **many)
 
 
 @gpu

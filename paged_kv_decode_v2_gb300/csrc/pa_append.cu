@@ -34,9 +34,9 @@ namespace pa {
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
 constexpr int kAppendThreads = 128;
-constexpr int kAppendRounds = 4; // rows per thread in flight
+constexpr int kAppendRounds = 2; // rows per thread in flight
+constexpr int kAppendCtas = 8;   // per SM
 
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
@@ -58,24 +58,44 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
                       E::pack(x[6], x[7]));
 }
 
-// The sequence of token row t: the number of entries of starts[0 .. n]
-// (non-decreasing) that are <= t, less one; -1 or n when t is in none.  The
-// warp probes 32 entries at a time: one round for up to 32 sequences, two for
-// 1024.
-__device__ __forceinline__ int find_seq(const int32_t *starts, int n, int t, int lane)
+// A sequence of a ragged batch: its token rows [begin, end) and its length.
+struct Seq {
+    int b, begin, end, len;
+};
+
+// The last sequence b < n whose key(b) <= at, key increasing with b: from its first
+// token row (key = starts[b]) or its first block item.  False when there is none.
+// The warp probes 32 entries at a time, and fetches the rows' ends and the lengths
+// along with the last probes: one chain link for up to 31 sequences, two for about
+// a thousand.
+template <typename Key>
+__device__ __forceinline__ bool find_seq(const AppendParams &p, long long at, int lane, Key key, Seq &s)
 {
-    int lo = 0, hi = n + 1; // the count is in [lo, hi]
-    while (lo < hi) {
+    const int n = p.num_seqs;
+    int lo = 0, hi = n; // how many have key <= at: in [lo, hi]
+    while (hi - lo > 30) {
         const int step = (hi - lo + 31) / 32;
-        const int at = lo + (lane + 1) * step - 1;
-        const bool le = at < hi && __ldg(starts + at) <= t;
+        const int i = lo + (lane + 1) * step - 1;
+        const bool le = i < hi && key(i, __ldg(p.token_starts + i)) <= at;
         const int c = __popc(__ballot_sync(0xffffffffu, le));
         const int next = min(lo + c * step, hi);
-        hi = min(hi, lo + (c + 1) * step - 1);
+        hi = max(min(hi, lo + (c + 1) * step - 1), next);
         lo = next;
-        hi = max(hi, lo);
     }
-    return lo - 1;
+    // Lane l holds entry first + l, first .. hi (at most 32 of them).
+    const int first = lo > 0 ? lo - 1 : 0;
+    const int i = first + lane;
+    const int start = i <= n && i <= hi ? __ldg(p.token_starts + i) : 0;
+    const int len = i < n && i <= hi ? __ldg(p.seq_lens + i) : 0;
+    const bool le = i < n && i < hi && key(i, start) <= at;
+    const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1; // among these
+    if (k < 0)
+        return false;
+    s.b = first + k;
+    s.begin = __shfl_sync(0xffffffffu, start, k);
+    s.end = __shfl_sync(0xffffffffu, start, k + 1);
+    s.len = __shfl_sync(0xffffffffu, len, k);
+    return true;
 }
 
 // Which two 8-dim chunks of a row item u (of head_dim / 16) covers, and
@@ -160,23 +180,22 @@ __device__ __forceinline__ void rotate_item(float (&x0)[8], float (&x1)[8], cons
 __device__ __forceinline__ bool place_of(const AppendParams &p, int t, int lane, bool reporter,
                                          int *seq, int *pos)
 {
-    int b, end;
+    Seq q;
     if (p.token_starts) {
-        b = find_seq(p.token_starts, p.num_seqs, t, lane);
-        if (b < 0 || b >= p.num_seqs)
-            return false;
-        end = __ldg(p.token_starts + b + 1);
-        if (end > p.num_tokens) {
+        if (!find_seq(p, t, lane, [](int, int start) { return (long long)start; }, q) || t >= q.end)
+            return false; // before the first sequence's rows or behind the last one's
+        if (q.end > p.num_tokens) {
             if (reporter)
                 set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
             return false;
         }
     } else {
-        b = t / p.q_len;
-        end = (b + 1) * p.q_len;
+        q.b = t / p.q_len;
+        q.end = (q.b + 1) * p.q_len;
+        q.len = __ldg(p.seq_lens + q.b);
     }
-    const int L = __ldg(p.seq_lens + b);
-    const long long at = (long long)L - end + t;
+    const int L = q.len;
+    const long long at = (long long)L - q.end + t;
     if (at < 0 || L > p.max_blocks * p.block_size) {
         if (reporter)
             set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
@@ -188,14 +207,14 @@ __device__ __forceinline__ bool place_of(const AppendParams &p, int t, int lane,
             set_status(p.status, PA_STATUS_BAD_POSITION);
         return false;
     }
-    *seq = b;
+    *seq = q.b;
     *pos = (int)at;
     return true;
 }
 
 // One CTA per token row; rows of heads: query, then key, then value.
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -344,13 +363,40 @@ __device__ __forceinline__ float amax8(const float (&x)[8], float m)
 // blocks: floor(x + n) - floor(x) >= floor(n)), else per sequence alike.
 __host__ __device__ inline int items_per_seq(int q_len, int bs) { return (q_len + bs - 2) / bs + 1; }
 
-// One CTA per (item, KV head), block_size * head_dim / 16 threads: thread =
-// (row of the block, pair of chunks).  CTAs past those rotate one token's
-// query rows each.
-template <typename T>
-__global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, int kv_ctas)
+// 16 codes of an earlier token's row, from scale `old` to scale `now`.
+__device__ __forceinline__ void requantise(uint2 *at, float old, float now)
 {
-    __shared__ float s_max[2][32];
+    if (now == old)
+        return;
+    uint4 *const q = reinterpret_cast<uint4 *>(at);
+    const uint4 v = *q;
+    const float f = old / now;
+    float x[8];
+    from_e4m3x8(make_uint2(v.x, v.y), x);
+    const uint2 a = to_e4m3x8(x, f);
+    from_e4m3x8(make_uint2(v.z, v.w), x);
+    const uint2 b = to_e4m3x8(x, f);
+    *q = make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// One CTA per item and `heads` KV heads, block_size * head_dim / 16 threads: thread
+// = (row of the block, pair of chunks).  CTAs past those rotate one token's query
+// rows each.  Several heads a CTA save the chain of loads that finds the block (and
+// the angles): prompts run 8 at a time, single tokens one, so that their CTAs fill
+// the GPU (see launch_append_q8).
+#ifndef AQ_T
+#define AQ_T 4
+#endif
+#ifndef AQ_H
+#define AQ_H 8
+#endif
+#ifndef AQ_MB
+#define AQ_MB 4
+#endif
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : AQ_MB) append_q8_kernel(const AppendParams p, int kv_ctas, int heads)
+{
+    __shared__ float s_max[2][64];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
@@ -359,24 +405,19 @@ __global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, i
     const int row = threadIdx.x / items;
     const bool interleaved = p.interleaved != 0;
     const Item rot = item_of(u, p.rotary_dim, interleaved, true);
-    const Item raw = item_of(u, 0, false, false);
     const int chunks = p.head_dim / 8;
-    float c[8], s[8];
+    float c[8] = {}, s[8] = {};
 
     if ((int)blockIdx.x >= kv_ctas) {
         // ---- one token's query rows
         const int t = blockIdx.x - kv_ctas;
-        int b, pos;
-        if (!place_of(p, t, lane, false, &b, &pos))
-            return;
         const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) +
                                                          t * p.query_stride);
         uint4 *qo = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) +
                                               t * p.query_out_stride);
-        if (p.rotary_dim)
-            load_angles(p.cos_sin + (size_t)pos * p.rotary_dim, rot, p.rotary_dim, interleaved, c, s);
         const int step = blockDim.x / items;
-        for (int base = row; base < p.num_heads; base += 2 * step) {
+        bool placed = false;
+        for (int base = row; base - row < p.num_heads; base += 2 * step) {
             uint4 x0[2], x1[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -384,6 +425,15 @@ __global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, i
                     x0[i] = q[(base + i * step) * chunks + rot.c0];
                     x1[i] = q[(base + i * step) * chunks + rot.c1];
                 }
+            if (!placed) {
+                placed = true;
+                int b, pos;
+                if (!place_of(p, t, lane, false, &b, &pos))
+                    return;
+                if (p.rotary_dim)
+                    load_angles(p.cos_sin + (size_t)pos * p.rotary_dim, rot, p.rotary_dim,
+                                interleaved, c, s);
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (base + i * step < p.num_heads) {
@@ -398,46 +448,37 @@ __global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, i
         return;
     }
 
-    // ---- one block of one KV head
-    const int item = blockIdx.x / p.num_kv_heads;
-    const int kv = blockIdx.x % p.num_kv_heads;
+    // ---- one block of `heads` KV heads, one after another
+    const int splits = (p.num_kv_heads + heads - 1) / heads;
+    const int item = blockIdx.x / splits;
+    const int kv0 = ((int)blockIdx.x - item * splits) * heads;
+    const int kv1 = min(kv0 + heads, p.num_kv_heads);
     const int bs = p.block_size;
-    int b, j, begin, end;
+    Seq q;
+    int j;
     if (p.token_starts) {
-        // The last sequence whose first item is at or before this one.
-        int lo = 0, hi = p.num_seqs;
-        while (lo < hi) {
-            const int step = (hi - lo + 31) / 32;
-            const int at = lo + (lane + 1) * step - 1;
-            const bool le =
-                at < hi && (long long)__ldg(p.token_starts + at) / bs + 2LL * at <= item;
-            const int n = __popc(__ballot_sync(0xffffffffu, le));
-            const int next = min(lo + n * step, hi);
-            hi = max(min(hi, lo + (n + 1) * step - 1), next);
-            lo = next;
-        }
-        b = lo - 1;
-        if (b < 0)
+        auto first_item = [&](int i, int start) { return (long long)start / bs + 2LL * i; };
+        if (!find_seq(p, item, lane, first_item, q))
             return;
-        begin = __ldg(p.token_starts + b);
-        end = __ldg(p.token_starts + b + 1);
-        j = item - (begin / bs + 2 * b);
+        j = item - (int)first_item(q.b, q.begin);
     } else {
         const int per = items_per_seq(p.q_len, bs);
-        b = item / per;
-        j = item % per;
-        begin = b * p.q_len;
-        end = begin + p.q_len;
+        q.b = item / per;
+        j = item - q.b * per;
+        q.begin = q.b * p.q_len;
+        q.end = q.begin + p.q_len;
+        q.len = __ldg(p.seq_lens + q.b);
     }
+    const int b = q.b, begin = q.begin, end = q.end;
     if (begin >= end || j < 0)
         return;
-    const bool reporter = threadIdx.x == 0 && kv == 0;
+    const bool reporter = threadIdx.x == 0 && kv0 == 0;
     if (begin < 0 || end > p.num_tokens) {
         if (reporter)
             set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
         return;
     }
-    const int L = __ldg(p.seq_lens + b);
+    const int L = q.len;
     const long long first = (long long)L - (end - begin); // position of the first new token
     const long long cap = (long long)p.max_blocks * bs;
     if (first < 0 || L > cap) {
@@ -466,89 +507,85 @@ __global__ void __launch_bounds__(1024) append_q8_kernel(const AppendParams p, i
         return;
     }
     const bool is_new = row >= new_lo && row < new_hi;
-    const size_t slot = (size_t)block * p.num_kv_heads + kv;
-    // Rows below new_lo hold earlier tokens: their scale is a floor.
-    const float old_k = new_lo > 0 ? __ldg(p.k_scales + slot) : 0.f;
-    const float old_v = new_lo > 0 ? __ldg(p.v_scales + slot) : 0.f;
-    float k0[8], k1[8];
-    uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-    float mk = 0.f, mv = 0.f;
+    const size_t slot0 = (size_t)block * p.num_kv_heads;
+    // This thread's two chunks of K and of V; the next head's are loaded while this
+    // one's maxima are found.
+    const Item raw = item_of(u, 0, false, false);
+    const uint4 *ksrc = nullptr, *vsrc = nullptr;
+    uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
     if (is_new) {
         const int t = begin + (int)(p0 + row - first);
-        const uint4 *ksrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) +
-                                                            t * p.key_stride) + kv * chunks;
-        const uint4 *vsrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) +
-                                                            t * p.value_stride) + kv * chunks;
-        const uint4 a = ksrc[rot.c0], d = ksrc[rot.c1];
-        v0 = vsrc[raw.c0];
-        v1 = vsrc[raw.c1];
+        ksrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) + t * p.key_stride);
+        vsrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) + t * p.value_stride);
+        k0 = __ldcs(ksrc + kv0 * chunks + rot.c0);
+        k1 = __ldcs(ksrc + kv0 * chunks + rot.c1);
+        v0 = __ldcs(vsrc + kv0 * chunks + raw.c0);
+        v1 = __ldcs(vsrc + kv0 * chunks + raw.c1);
         if (p.rotary_dim)
             load_angles(p.cos_sin + (size_t)(p0 + row) * p.rotary_dim, rot, p.rotary_dim,
                         interleaved, c, s);
-        unpack8<T>(a, k0);
-        unpack8<T>(d, k1);
-        rotate_item(k0, k1, rot, interleaved, c, s);
-        mk = amax8(k1, amax8(k0, 0.f));
-        float x[8];
-        unpack8<T>(v0, x);
-        mv = amax8(x, 0.f);
-        unpack8<T>(v1, x);
-        mv = amax8(x, mv);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
-    }
-    if (lane == 0) {
-        s_max[0][threadIdx.x >> 5] = mk;
-        s_max[1][threadIdx.x >> 5] = mv;
-    }
-    __syncthreads();
     const int warps = blockDim.x >> 5;
-    mk = lane < warps ? s_max[0][lane] : 0.f;
-    mv = lane < warps ? s_max[1][lane] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
-    }
-    const float sk = fmaxf(scale_of(mk), old_k), sv = fmaxf(scale_of(mv), old_v);
-    if (threadIdx.x == 0) {
-        p.k_scales[slot] = sk;
-        p.v_scales[slot] = sv;
-    }
-    uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) +
-                                          (slot * bs + row) * p.head_dim);
-    uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) +
-                                          (slot * bs + row) * p.head_dim);
-    if (is_new) {
-        // x / s is x times an exact power of two for the scales this writes.
-        float x[8];
-        const float fk = 1.f / sk, fv = 1.f / sv;
-        kd[rot.c0] = to_e4m3x8(k0, fk);
-        kd[rot.c1] = to_e4m3x8(k1, fk);
-        unpack8<T>(v0, x);
-        vd[raw.c0] = to_e4m3x8(x, fv);
-        unpack8<T>(v1, x);
-        vd[raw.c1] = to_e4m3x8(x, fv);
-    } else if (row < new_lo) {
-        float x[8];
-        if (sk != old_k) {
-            const float f = old_k / sk;
-            const uint2 a = kd[raw.c0], d = kd[raw.c1];
-            from_e4m3x8(a, x);
-            kd[raw.c0] = to_e4m3x8(x, f);
-            from_e4m3x8(d, x);
-            kd[raw.c1] = to_e4m3x8(x, f);
+    for (int kv = kv0; kv < kv1; ++kv) {
+        const size_t slot = slot0 + kv;
+        // Rows below new_lo hold earlier tokens: their scale is a floor.
+        const float old_k = new_lo > 0 ? __ldg(p.k_scales + slot) : 0.f;
+        const float old_v = new_lo > 0 ? __ldg(p.v_scales + slot) : 0.f;
+        float a[8], d[8];
+        unpack8<T>(k0, a);
+        unpack8<T>(k1, d);
+        rotate_item(a, d, rot, interleaved, c, s);
+        const uint4 w0 = v0, w1 = v1;
+        if (is_new && kv + 1 < kv1) {
+            k0 = __ldcs(ksrc + (kv + 1) * chunks + rot.c0);
+            k1 = __ldcs(ksrc + (kv + 1) * chunks + rot.c1);
+            v0 = __ldcs(vsrc + (kv + 1) * chunks + raw.c0);
+            v1 = __ldcs(vsrc + (kv + 1) * chunks + raw.c1);
         }
-        if (sv != old_v) {
-            const float f = old_v / sv;
-            const uint2 a = vd[raw.c0], d = vd[raw.c1];
-            from_e4m3x8(a, x);
-            vd[raw.c0] = to_e4m3x8(x, f);
-            from_e4m3x8(d, x);
-            vd[raw.c1] = to_e4m3x8(x, f);
+        float mk = amax8(d, amax8(a, 0.f)), mv;
+        {
+            float x[8];
+            unpack8<T>(w0, x);
+            mv = amax8(x, 0.f);
+            unpack8<T>(w1, x);
+            mv = amax8(x, mv);
+        }
+        // Non-negative floats order as their bits.
+        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+        float *const sm = s_max[kv & 1]; // the head before may still be reading the other half
+        if (lane == 0) {
+            sm[threadIdx.x >> 5] = mk;
+            sm[32 + (threadIdx.x >> 5)] = mv;
+        }
+        __syncthreads();
+        mk = lane < warps ? sm[lane] : 0.f;
+        mv = lane < warps ? sm[32 + lane] : 0.f;
+        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+        const float sk = fmaxf(scale_of(mk), old_k), sv = fmaxf(scale_of(mv), old_v);
+        if (threadIdx.x == 0) {
+            p.k_scales[slot] = sk;
+            p.v_scales[slot] = sv;
+        }
+        uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) +
+                                              (slot * bs + row) * p.head_dim);
+        uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) +
+                                              (slot * bs + row) * p.head_dim);
+        if (is_new) {
+            // x / s is x times an exact power of two for the scales this writes.
+            const float fk = 1.f / sk, fv = 1.f / sv;
+            kd[rot.c0] = to_e4m3x8(a, fk);
+            kd[rot.c1] = to_e4m3x8(d, fk);
+            float x[8];
+            unpack8<T>(w0, x);
+            const uint2 e = to_e4m3x8(x, fv);
+            unpack8<T>(w1, x);
+            const uint2 f = to_e4m3x8(x, fv);
+            *reinterpret_cast<uint4 *>(vd + raw.c0) = make_uint4(e.x, e.y, f.x, f.y);
+        } else if (row < new_lo) {
+            requantise(kd + raw.c0, old_k, sk);
+            requantise(vd + raw.c0, old_v, sv);
         }
     }
 }
@@ -590,15 +627,37 @@ long long append_q8_ctas(const AppendParams &p)
     return append_q8_items(p) * p.num_kv_heads + (p.num_heads ? p.num_tokens : 0);
 }
 
-cudaError_t launch_append_q8(int dtype, const AppendParams &p, cudaStream_t stream)
+cudaError_t launch_append_q8(int dtype, const AppendParams &p, int num_sms, cudaStream_t stream)
 {
-    int kv_ctas = (int)(append_q8_items(p) * p.num_kv_heads);
-    void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas};
+    // KV heads of a CTA: as many as leave some eight CTAs per SM (counting the items
+    // that hold tokens: at most every block of a prompt, and one per sequence).
+    const long long items = append_q8_items(p);
+    const long long used = (long long)p.num_tokens / p.block_size + p.num_seqs;
+    int heads = (int)(used * p.num_kv_heads / (8LL * num_sms));
+    heads = heads < 1 ? 1 : heads > AQ_H ? AQ_H : heads;
+    heads = heads > p.num_kv_heads ? p.num_kv_heads : heads;
+    const int splits = (p.num_kv_heads + heads - 1) / heads;
+    // Many tokens' queries go to the 16-bit kernel behind this one (more of them in
+    // flight); few share this launch.
+    const bool apart = p.num_heads && p.num_tokens >= AQ_T * num_sms;
+    int kv_ctas = (int)(items * splits);
+    void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas, &heads};
     const unsigned threads = (unsigned)(p.block_size * p.head_dim / 16);
-    const unsigned grid = (unsigned)append_q8_ctas(p);
-    return dtype == PA_BF16
-               ? launch_pdl(&append_q8_kernel<__nv_bfloat16>, grid, threads, stream, args)
-               : launch_pdl(&append_q8_kernel<__half>, grid, threads, stream, args);
+    const unsigned grid = (unsigned)(kv_ctas + (p.num_heads && !apart ? p.num_tokens : 0));
+    cudaError_t e;
+    if (threads <= 256)
+        e = dtype == PA_BF16
+                ? launch_pdl(&append_q8_kernel<__nv_bfloat16, false>, grid, threads, stream, args)
+                : launch_pdl(&append_q8_kernel<__half, false>, grid, threads, stream, args);
+    else
+        e = dtype == PA_BF16
+                ? launch_pdl(&append_q8_kernel<__nv_bfloat16, true>, grid, threads, stream, args)
+                : launch_pdl(&append_q8_kernel<__half, true>, grid, threads, stream, args);
+    if (e != cudaSuccess || !apart)
+        return e;
+    AppendParams q = p;
+    q.num_kv_heads = 0;
+    return launch_append(dtype, q, stream);
 }
 
 } // namespace pa

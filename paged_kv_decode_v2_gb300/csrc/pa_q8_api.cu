@@ -25,17 +25,17 @@ int rows_per_cta(int cols, int head_dim)
     return cols <= 32 || head_dim == 256 ? 32 : 64;
 }
 
-std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
+std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2];
 
-int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
+int launch_tc(Q8Launch &L, int dev, int sms, int nr, cudaStream_t stream, int *ctas)
 {
-    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype, L.v1);
+    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype);
     if (!k.fn)
         return PA_ERR_UNSUPPORTED;
     const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
     const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
     std::atomic<int> &cell =
-        g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
+        g_tc_limit[dev][(di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)];
     // Dynamic limit after the opt-in in the low 18 bits, static bytes above them.
     int have = cell.load(std::memory_order_acquire);
     if (have == 0) {
@@ -58,12 +58,17 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
     // As many CTAs per SM as the kernel is made for, if rings of two stages fit.
     const size_t sm = limit + fixed_static + 1024; // a CTA also takes 1 KB for the system
     size_t per_cta = limit;
+    int per_sm = 1;
     for (int n = k.ctas; n > 1; --n) {
         if (k.fixed_bytes + 4 * tile + fixed_static + 1024 <= sm / n) {
             per_cta = sm / n - 1024 - fixed_static;
+            per_sm = n;
             break;
         }
     }
+    if (L.p.stream)
+        L.grid = dim3((unsigned)(per_sm * sms));
+    *ctas = per_sm * sms;
     int ks = 1, vs = 1;
     while (k.fixed_bytes + (ks + vs + 1) * tile <= per_cta && ks + vs < 2 * kMaxStages) {
         if (ks > vs)
@@ -222,7 +227,11 @@ int append_impl(const void *key, const void *value, int64_t key_stride, int64_t 
         return PA_OK;
     if (q8 && append_q8_ctas(p) > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    const cudaError_t e = q8 ? launch_append_q8(dtype, p, stream) : launch_append(dtype, p, stream);
+    int dev, sms;
+    if (host_device(&dev, &sms))
+        return PA_ERR_CUDA;
+    const cudaError_t e =
+        q8 ? launch_append_q8(dtype, p, sms, stream) : launch_append(dtype, p, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -233,19 +242,18 @@ int row_groups(int cols, int head_dim)
     return (cols + nr - 1) / nr;
 }
 
-// The partition size pa_decode_q8 runs V2 with, or 0 for V1.
-int choose_partition(int num_seqs, int q_len, int group, int num_kv_heads, int head_dim,
-                     int max_seq_len, int partition_size, int sms)
+// Whether the work is cut into equal stretches (else one CTA per group), and the
+// tiles q_min a stretch has at least, so that a group's partials, at most (n - 1) / q
+// + 2 for its n tiles, fit the np the intermediates have room for.
+bool choose_stream(int num_seqs, long long groups, int cap, int np, int sms, int *q_min)
 {
-    const int np = pa_v2_num_partitions(max_seq_len, partition_size);
-    const long long v1_ctas = (long long)num_seqs * num_kv_heads * row_groups(q_len * group, head_dim);
-    if (np <= 1 || (np == 2 && v1_ctas <= sms))
-        return 0;
-    // Twice the partition while the grid still gives every SM its CTAs.
-    long long pc = partition_size;
-    while (pc < 1024 && v1_ctas * pa_v2_num_partitions(max_seq_len, (int)(2 * pc)) >= 6LL * sms)
-        pc *= 2;
-    return pa_v2_num_partitions(max_seq_len, (int)pc) <= 1 ? 0 : (int)pc;
+    const long long n = ((long long)cap + kQ8Tok - 1) / kQ8Tok;
+    // A single partial, or two on a grid that leaves every SM at most one CTA: the
+    // merge's launch would cost more than splitting gains.
+    if (np <= 1 || (np == 2 && groups <= sms) || num_seqs > kQ8Seqs || n * groups > INT32_MAX)
+        return false;
+    *q_min = (int)((n - 1) / (np - 1)) + 1;
+    return true;
 }
 
 // ---- the 16-bit copy for many rows
@@ -316,15 +324,6 @@ bool plan_copy(CopyPlan &plan, Q8CopyParams &c, const Q8Params &p, int partition
     return true;
 }
 
-int check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
-                 int max_seq_len, int partition_size)
-{
-    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
-        return PA_ERR_INVALID_ARG;
-    return PA_OK;
-}
-
 } // namespace
 
 extern "C" {
@@ -365,18 +364,6 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
                        (cudaStream_t)stream);
 }
 
-PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
-                                  int head_dim, int max_seq_len, int partition_size)
-{
-    if (check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len, partition_size))
-        return -PA_ERR_INVALID_ARG;
-    int dev, sms;
-    if (host_device(&dev, &sms))
-        return -PA_ERR_CUDA;
-    return choose_partition(num_seqs, q_len, num_heads / num_kv_heads, num_kv_heads, head_dim,
-                            max_seq_len, partition_size, sms);
-}
-
 PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *value_cache,
                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
                         const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
@@ -410,12 +397,14 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     const bool work_ok = tmp_output && exp_sums && max_logits && max_num_partitions > 0 &&
                          host_aligned(tmp_output, 16) && host_aligned(exp_sums, 4) &&
                          host_aligned(max_logits, 4);
-    const int part =
-        choose_partition(num_seqs, q_len, group, num_kv_heads, head_dim, cap, partition_size, sms);
-    const int np = part ? pa_v2_num_partitions(cap, part) : 1;
-    if (part && !work_ok)
+    const int np = pa_v2_num_partitions(cap, partition_size);
+    const int col_groups = row_groups(group * q_len, head_dim);
+    int q_min = 1;
+    const bool streamed =
+        choose_stream(num_seqs, (long long)num_seqs * num_kv_heads * col_groups, cap, np, sms, &q_min);
+    if (streamed && !work_ok)
         return PA_ERR_INVALID_ARG;
-    if (part && np > max_num_partitions)
+    if (streamed && np > max_num_partitions)
         return PA_ERR_WORKSPACE;
 
     Q8Launch L = {};
@@ -437,13 +426,15 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.group = group;
     p.q_len = q_len;
     p.cols = group * q_len;
-    p.col_groups = row_groups(p.cols, head_dim);
+    p.col_groups = col_groups;
     p.num_blocks = num_blocks;
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
     p.max_blocks = max_blocks_per_seq;
     p.seq_len_cap = cap;
     p.scale = scale;
-    p.partition_size = part;
+    p.stream = streamed;
+    p.num_seqs = num_seqs;
+    p.q_min = q_min;
     p.max_num_partitions = max_num_partitions;
     p.tmp_output = tmp_output;
     p.exp_sums = exp_sums;
@@ -452,7 +443,6 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.status = status;
     L.head_dim = head_dim;
     L.block_size = block_size;
-    L.v1 = part == 0;
 
     if (work_ok && p.cols >= kQ8CopyRows) {
         Q8CopyParams c = {};
@@ -468,23 +458,22 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
                                    plan.np, dtype, out, tmp_output, exp_sums, max_logits, status, st);
             if (rc || !plan.may_flag)
                 return rc;
-            // Values that binary16 cannot hold: the 8-bit kernel runs after all (V1,
-            // which needs no intermediates, over the result above).
+            // Values that binary16 cannot hold: the 8-bit kernel runs after all (a CTA
+            // per group, which needs no intermediates, over the result above).
             p.only_if = c.flag;
-            L.v1 = true;
-            p.partition_size = 0;
+            p.stream = 0;
         }
     }
-    // Column groups of one partition are adjacent in x: their reads meet in L2.
-    const long long gx = (long long)(L.v1 ? 1 : np) * p.col_groups;
-    if (gx > INT32_MAX)
-        return PA_ERR_UNSUPPORTED;
-    L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
-    rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);
-    if (rc || L.v1)
+    // Row tiles of one KV head are neighbours: their reads meet in L2.
+    L.grid = dim3(col_groups, num_kv_heads, num_seqs);
+    int ctas = 0;
+    rc = launch_tc(L, dev, sms, rows_per_cta(p.cols, head_dim), st, &ctas);
+    if (rc || !p.stream)
         return rc;
-    return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
-                      exp_sums, max_logits, max_num_partitions, out, status, st);
+    const StreamPlan plan = {num_seqs, num_kv_heads, col_groups, rows_per_cta(p.cols, head_dim),
+                             kQ8Tok,   ctas,         q_min};
+    return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, partition_size, dtype,
+                      tmp_output, exp_sums, max_logits, max_num_partitions, out, plan, status, st);
 }
 
 } // extern "C"

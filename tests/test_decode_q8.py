@@ -36,12 +36,6 @@ def test_refused_before_launch(cuda_lib, kw, code):
     assert _call(cuda_lib.load(), **kw) == code
 
 
-def test_partition_arguments(cuda_lib):
-    for bad in ((0, 1, 8, 2, 128, 1000, 512), (1, 0, 8, 2, 128, 1000, 512), (1, 1, 7, 2, 128, 1000, 512),
-                (1, 1, 8, 2, 0, 1000, 512), (1, 1, 8, 2, 128, -1, 512), (1, 1, 8, 2, 128, 1000, 0)):
-        assert cuda_lib.load().pa_decode_q8_partition(*bad) == -1
-
-
 def test_binding_refuses(cuda_lib):
     kc, vc, ks, vs, tables, lens = cu.cache8([40, 3])
     q = torch.zeros((2, 4, 64), dtype=F16)
@@ -210,14 +204,6 @@ def test_same_bits_every_time_and_under_a_graph(pa, Q, G):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
-
-
-@gpu
-def test_partitions_never_finer(pa):
-    for S, Q, H, KV, L, P in ((1, 1, 32, 4, 100000, 512), (32, 1, 32, 8, 8192, 512), (32, 16, 32, 8, 8192, 512),
-                              (2, 2048, 32, 8, 32768, 512), (1, 1, 8, 2, 1000, 512), (64, 1, 64, 8, 32768, 1000)):
-        p = pa.pa_decode_q8_partition(S, Q, H, KV, 128, L, P)
-        assert p == 0 or p >= P
 
 
 @gpu

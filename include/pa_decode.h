@@ -511,12 +511,11 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  * (q_len > 1, the same causal rule) with
  *     K_t = k_scales[block of t][k] * key_cache[...],   V_t likewise.
  * dtype is the type of query and out; the other arguments are pa_decode_mq's.
- * The work is cut as the lengths and the GPU ask: partition_size says only how
- * much room the intermediates have, max_num_partitions >= ceil(max_seq_len /
- * partition_size) per row (max_seq_len as for pa_decode), PA_ERR_WORKSPACE
- * otherwise.  Their contents afterwards are unspecified.  A call with room for
- * one partition (or two, and at most one (sequence, KV head, row tile) group
- * per SM) and one of more than 512 sequences uses no intermediates.
+ * Picks V1 or V2 itself, V2 at the partition size pa_decode_q8_partition
+ * returns for (num_seqs, q_len, num_heads, num_kv_heads, head_dim,
+ * max_seq_len_hint if > 0 else max_blocks_per_seq * block_size,
+ * partition_size).  The intermediates must be valid whenever V2 can be chosen;
+ * their contents after the call are unspecified.
  *
  * From 256 query rows (q_len * G) per KV head on, when tmp_output has room for
  * it, the call first makes a 16-bit copy of the blocks that it reads there (in
@@ -542,6 +541,15 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
                         int partition_size, int dtype, void *out, float *tmp_output,
                         float *exp_sums, float *max_logits, int max_num_partitions,
                         int32_t *status, pa_stream_t stream);
+
+/*
+ * The partition size pa_decode_q8 runs V2 with for these sizes on the current
+ * device: at least partition_size (intermediates sized for partition_size
+ * always suffice), or 0 when it runs V1.  Negative PA_ERR_* code for invalid
+ * arguments.  Host only.
+ */
+PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                  int head_dim, int max_seq_len, int partition_size);
 
 /*
  * Size of the intermediates array that pa_decode_v2_static keeps inside the

@@ -88,6 +88,8 @@ def load() -> ctypes.CDLL:
     lib.pa_decode_q8.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P, P, P,
                                  P, I, P, P]
     lib.pa_decode_q8.restype = I
+    lib.pa_decode_q8_partition.argtypes = [I, I, I, I, I, I, I]
+    lib.pa_decode_q8_partition.restype = I
     lib.pa_status_string.argtypes = [I]
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_set_launch_config.argtypes = [I, I]
@@ -538,3 +540,13 @@ def pa_decode_q8(query, key_cache, value_cache, k_scales, v_scales, block_tables
            nb, bs, mb, max_seq_len_hint, scale, partition_size, _DTYPE[dtype], out.data_ptr(),
            _addr(tmp_output), _addr(exp_sums), _addr(max_logits), parts, _addr(status)])
     return out
+
+
+def pa_decode_q8_partition(num_seqs: int, q_len: int, num_heads: int, num_kv_heads: int,
+                           head_dim: int, max_seq_len: int, partition_size: int) -> int:
+    """Partition size pa_decode_q8 runs V2 with (0 when it runs V1)."""
+    r = load().pa_decode_q8_partition(num_seqs, q_len, num_heads, num_kv_heads, head_dim,
+                                      max_seq_len, partition_size)
+    if r < 0:
+        raise PagedAttentionError("pa_decode_q8_partition", -r)
+    return r

@@ -384,17 +384,9 @@ __device__ __forceinline__ void requantise(uint2 *at, float old, float now)
 // rows each.  Several heads a CTA save the chain of loads that finds the block (and
 // the angles): prompts run 8 at a time, single tokens one, so that their CTAs fill
 // the GPU (see launch_append_q8).
-#ifndef AQ_T
-#define AQ_T 4
-#endif
-#ifndef AQ_H
-#define AQ_H 8
-#endif
-#ifndef AQ_MB
-#define AQ_MB 4
-#endif
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : AQ_MB) append_q8_kernel(const AppendParams p, int kv_ctas, int heads)
+__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
+    append_q8_kernel(const AppendParams p, int kv_ctas, int heads)
 {
     __shared__ float s_max[2][64];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -627,6 +619,9 @@ long long append_q8_ctas(const AppendParams &p)
     return append_q8_items(p) * p.num_kv_heads + (p.num_heads ? p.num_tokens : 0);
 }
 
+constexpr int kMaxHeads = 8;     // KV heads of a CTA at most
+constexpr int kApartTokens = 60; // tokens per SM from which queries get their own launch
+
 cudaError_t launch_append_q8(int dtype, const AppendParams &p, int num_sms, cudaStream_t stream)
 {
     // KV heads of a CTA: as many as leave some eight CTAs per SM (counting the items
@@ -634,12 +629,12 @@ cudaError_t launch_append_q8(int dtype, const AppendParams &p, int num_sms, cuda
     const long long items = append_q8_items(p);
     const long long used = (long long)p.num_tokens / p.block_size + p.num_seqs;
     int heads = (int)(used * p.num_kv_heads / (8LL * num_sms));
-    heads = heads < 1 ? 1 : heads > AQ_H ? AQ_H : heads;
+    heads = heads < 1 ? 1 : heads > kMaxHeads ? kMaxHeads : heads;
     heads = heads > p.num_kv_heads ? p.num_kv_heads : heads;
     const int splits = (p.num_kv_heads + heads - 1) / heads;
     // Many tokens' queries go to the 16-bit kernel behind this one (more of them in
     // flight); few share this launch.
-    const bool apart = p.num_heads && p.num_tokens >= AQ_T * num_sms;
+    const bool apart = p.num_heads && p.num_tokens >= kApartTokens * num_sms;
     int kv_ctas = (int)(items * splits);
     void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas, &heads};
     const unsigned threads = (unsigned)(p.block_size * p.head_dim / 16);

@@ -74,18 +74,6 @@ struct AttnLaunch {
     size_t smem_bytes;
 };
 
-// How the 8-bit attention cut its work (pa_q8_tc.cuh): groups (sequence, KV head,
-// row tile) of one tile order, CTA c taking tiles [c q, (c + 1) q).
-struct StreamPlan {
-    int num_seqs;                // 0: partitions of partition_size tokens instead
-    int num_kv_heads;
-    int col_groups;              // row tiles per KV head
-    int rows;                    // rows of a row tile
-    int tile;                    // tokens of a tile
-    int ctas;
-    int q_min;
-};
-
 struct MergeParams {
     const int32_t *seq_lens;
     int q_len;                   // rows of the grid's y dimension are (sequence, new token)
@@ -99,7 +87,6 @@ struct MergeParams {
     const float *max_logits;
     void *out;
     int32_t *status;
-    StreamPlan plan;
 };
 
 // The binary16 copy of the V blocks a multi-query call reads (bf16 caches):

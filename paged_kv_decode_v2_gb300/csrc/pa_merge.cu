@@ -38,37 +38,7 @@ __device__ __forceinline__ void merge_state(float &m, float &l, float4 &a, float
     m = M;
 }
 
-// Partials of (sequence b, new token i, head h) under a stream plan: its group's
-// tiles [s, s + n) lie in CTAs s / q to (s + n - 1) / q.  0 for an empty sequence.
-// Whole warps call it; lanes share the sum over the sequences.
-__device__ __forceinline__ int stream_parts(const MergeParams &p, int b, int i, int h)
-{
-    const StreamPlan &sp = p.plan;
-    auto tiles = [&](int s) -> int {
-        int L = __ldg(&p.seq_lens[s]);
-        L = L < 0 ? 0 : (L > p.seq_len_cap ? p.seq_len_cap : L);
-        return (int)(((long long)L + sp.tile - 1) / sp.tile);
-    };
-    int before = 0, all = 0;
-    for (int s = threadIdx.x & 31; s < sp.num_seqs; s += 32) {
-        const int n = tiles(s);
-        before += s < b ? n : 0;
-        all += n;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    all = __reduce_add_sync(0xffffffffu, all);
-    const int n = tiles(b);
-    if (n == 0)
-        return 0;
-    const int kr = sp.num_kv_heads * sp.col_groups;
-    const int q = max((all * kr + sp.ctas - 1) / sp.ctas, sp.q_min);
-    const int group = p.num_heads / sp.num_kv_heads;
-    const int rt = sp.col_groups == 1 ? 0 : (i * group + h % group) / sp.rows;
-    const int start = before * kr + ((h / group) * sp.col_groups + rt) * n;
-    return (start + n - 1) / q - start / q + 1;
-}
-
-template <typename T, int DD, int NTH, bool STREAM>
+template <typename T, int DD, int NTH>
 __global__ void __launch_bounds__(NTH) merge_kernel(const MergeParams p)
 {
     using E = Elem<T>;
@@ -93,16 +63,9 @@ __global__ void __launch_bounds__(NTH) merge_kernel(const MergeParams p)
     // waits for this grid's completion before it touches global memory.
     asm volatile("griddepcontrol.launch_dependents;");
     // Inputs not written by phase 1 may be read before the dependency wait.
-    int np;
-    if constexpr (STREAM) {
-        np = stream_parts(p, b, row - b * p.q_len, h);
-        if (np == 1)
-            return; // written by the attention kernel
-    } else {
-        int L = __ldg(&p.seq_lens[b]);
-        L = L < 0 ? 0 : (L > p.seq_len_cap ? p.seq_len_cap : L);
-        np = (L + p.partition_size - 1) / p.partition_size;
-    }
+    int L = __ldg(&p.seq_lens[b]);
+    L = L < 0 ? 0 : (L > p.seq_len_cap ? p.seq_len_cap : L);
+    const int np = (L + p.partition_size - 1) / p.partition_size;
     const size_t bh = (size_t)row * p.num_heads + h;
     T *out = static_cast<T *>(p.out) + bh * D + d0;
     if (np == 0) {
@@ -179,7 +142,7 @@ __global__ void __launch_bounds__(NTH) merge_kernel(const MergeParams p)
 // head) with row = pair / num_heads; lane l owns dims [l * DL, l * DL + DL).
 // The partitions are folded in index order with the same running-maximum
 // rule as the slice form.
-template <typename T, int D, bool STREAM>
+template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergeParams p, int pairs)
 {
     using E = Elem<T>;
@@ -193,16 +156,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergePa
         return;
     const int row = pair / p.num_heads;   // (sequence, new token) = b * q_len + i
     const int b = row / p.q_len;
-    int np;
-    if constexpr (STREAM) {
-        np = stream_parts(p, b, row - b * p.q_len, pair - row * p.num_heads);
-        if (np == 1)
-            return; // written by the attention kernel
-    } else {
-        int L = __ldg(&p.seq_lens[b]);
-        L = L < 0 ? 0 : (L > p.seq_len_cap ? p.seq_len_cap : L);
-        np = (L + p.partition_size - 1) / p.partition_size;
-    }
+    int L = __ldg(&p.seq_lens[b]);
+    L = L < 0 ? 0 : (L > p.seq_len_cap ? p.seq_len_cap : L);
+    const int np = (L + p.partition_size - 1) / p.partition_size;
     T *out = static_cast<T *>(p.out) + (size_t)pair * D + lane * DL;
     if (np == 0) {
 #pragma unroll
@@ -257,38 +213,26 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergePa
         out[j] = E::from_float(acc[j] * inv);
 }
 
-template <typename T, bool STREAM>
+template <typename T>
 static cudaError_t launch_rows_t(cudaLaunchConfig_t &cfg, int head_dim, const MergeParams &p,
                                  int pairs)
 {
     switch (head_dim) {
-    case 64: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 64, STREAM>, p, pairs);
-    case 256: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 256, STREAM>, p, pairs);
-    default: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 128, STREAM>, p, pairs);
+    case 64: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 64>, p, pairs);
+    case 256: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 256>, p, pairs);
+    default: return cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, 128>, p, pairs);
     }
 }
 
-template <typename T, bool STREAM>
+template <typename T>
 static cudaError_t launch_merge_t(cudaLaunchConfig_t &cfg, int dd, const MergeParams &p)
 {
     switch (dd) {
-    case 16: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 16, kMergeThreads, STREAM>, p);
-    case 32: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 32, kMergeThreads, STREAM>, p);
-    case 64: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 64, kMergeThreads, STREAM>, p);
-    default: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 128, kMergeThreads, STREAM>, p);
+    case 16: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 16, kMergeThreads>, p);
+    case 32: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 32, kMergeThreads>, p);
+    case 64: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 64, kMergeThreads>, p);
+    default: return cudaLaunchKernelEx(&cfg, merge_kernel<T, 128, kMergeThreads>, p);
     }
-}
-
-// Partials of the longest sequence; under a stream plan as if every sequence were
-// as long (shorter ones make the stretches shorter and its partials more).
-static int most_partials(const MergeParams &p, int num_seqs)
-{
-    const StreamPlan &sp = p.plan;
-    if (!sp.num_seqs)
-        return (p.seq_len_cap + p.partition_size - 1) / p.partition_size;
-    const long long n = ((long long)p.seq_len_cap + sp.tile - 1) / sp.tile;
-    const long long q = (n * num_seqs * sp.num_kv_heads * sp.col_groups + sp.ctas - 1) / sp.ctas;
-    return (int)(n / (q > sp.q_min ? q : sp.q_min)) + 2;
 }
 
 int merge_form(const MergeParams &p, int num_seqs, int num_sms, int forced)
@@ -309,7 +253,7 @@ int merge_form(const MergeParams &p, int num_seqs, int num_sms, int forced)
     // pairs); the same batch with one new token 142.5 / 143.6 (64 partitions,
     // 4K pairs); one 100K-token sequence 37.1 / 69.7; stress at 2 sequences
     // 159.5 / 179.0.
-    const int np_max = most_partials(p, num_seqs);
+    const int np_max = (p.seq_len_cap + p.partition_size - 1) / p.partition_size;
     const bool many = pairs > 16LL * num_sms && pairs <= (1LL << 30);
     return many && (np_max <= 8 || (np_max <= 32 && pairs >= 32LL * num_sms)) ? 2 : 1;
 }
@@ -330,7 +274,7 @@ cudaError_t launch_merge(int dtype, const MergeParams &p, int num_seqs, int num_
     // ragged batches 1.3 and 2.5 us instead, from not fitting beside the
     // attention kernel.
     const long long pairs = (long long)p.num_heads * num_seqs * p.q_len;
-    const int np_max = most_partials(p, num_seqs);
+    const int np_max = (p.seq_len_cap + p.partition_size - 1) / p.partition_size;
     int dd = p.head_dim < 128 ? p.head_dim : 128;
     while (dd > 16) {
         const long long ctas = pairs * (p.head_dim / dd);
@@ -357,19 +301,14 @@ cudaError_t launch_merge(int dtype, const MergeParams &p, int num_seqs, int num_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int n = (int)pairs_all;
-    if (p.plan.num_seqs) {
-        if (rows)
-            return dtype == PA_BF16 ? launch_rows_t<__nv_bfloat16, true>(cfg, p.head_dim, p, n)
-                                    : launch_rows_t<__half, true>(cfg, p.head_dim, p, n);
-        return dtype == PA_BF16 ? launch_merge_t<__nv_bfloat16, true>(cfg, dd, p)
-                                : launch_merge_t<__half, true>(cfg, dd, p);
+    if (rows) {
+        if (dtype == PA_BF16)
+            return launch_rows_t<__nv_bfloat16>(cfg, p.head_dim, p, (int)pairs_all);
+        return launch_rows_t<__half>(cfg, p.head_dim, p, (int)pairs_all);
     }
-    if (rows)
-        return dtype == PA_BF16 ? launch_rows_t<__nv_bfloat16, false>(cfg, p.head_dim, p, n)
-                                : launch_rows_t<__half, false>(cfg, p.head_dim, p, n);
-    return dtype == PA_BF16 ? launch_merge_t<__nv_bfloat16, false>(cfg, dd, p)
-                            : launch_merge_t<__half, false>(cfg, dd, p);
+    if (dtype == PA_BF16)
+        return launch_merge_t<__nv_bfloat16>(cfg, dd, p);
+    return launch_merge_t<__half>(cfg, dd, p);
 }
 
 // One warp waits on a barrier that nothing completes; the bounded wait must

@@ -24,7 +24,7 @@ void host_tuning(int *warps, int *stages, int *rows_kernel);
 int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
                int max_seq_len, int partition_size, int dtype, const float *tmp_output,
                const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
-               const StreamPlan &plan, int32_t *status, cudaStream_t stream);
+               int32_t *status, cudaStream_t stream);
 
 // The 16-bit multi-query attention over copies of K and V (partials at a stride
 // of np partitions of `part` tokens, V1 when part is 0), bf16 with V's binary16
@@ -101,16 +101,15 @@ struct Q8Params {
     int max_blocks;
     int seq_len_cap;
     float scale;
-    int stream;                  // work in equal stretches over the CTAs; else a CTA per group
-    int num_seqs;
-    int q_min;                   // tiles of a stretch at least
+    int partition_size;          // V2, and V1 over a cluster: tokens of a CTA
+    int ways;                    // V1: CTAs of a cluster that share a row tile's tokens
     int stages;                  // K ring stages
     int v_stages;                // V ring stages
-    int max_num_partitions;      // partials that the intermediates hold per row
-    float *tmp_output;
+    int max_num_partitions;      // V2: partition capacity of the intermediates
+    float *tmp_output;           // V2
     float *exp_sums;
     float *max_logits;
-    void *out;
+    void *out;                   // V1
     const int32_t *only_if;      // run only if this word is not 0 (null: always)
     int32_t *status;
 };
@@ -139,13 +138,14 @@ struct Q8Launch {
     CUtensorMap tmap_v;
     int head_dim;
     int block_size;
+    bool v1;
     dim3 grid;
     size_t smem_bytes;
 };
 
 // The tcgen05 kernels: one per (head_dim, rows per CTA), see pa_q8_tc.cuh.
 constexpr int kQ8Tok = 128; // tokens per tile
-constexpr int kQ8Seqs = 512; // sequences whose lengths a CTA holds (streamed work)
+constexpr int kQ8Ways = 8;  // CTAs of a cluster at most (the portable size)
 struct Q8TcKernel {
     const void *fn;
     int threads;
@@ -153,15 +153,15 @@ struct Q8TcKernel {
     size_t fixed_bytes;      // dynamic shared memory but for the rings
 };
 // rows 8, 16, 32, or (up to head_dim 128) 64; fn null otherwise.
-Q8TcKernel q8_tc_d64(int rows, int dtype);
-Q8TcKernel q8_tc_d128(int rows, int dtype);
-Q8TcKernel q8_tc_d256(int rows, int dtype);
+Q8TcKernel q8_tc_d64(int rows, int dtype, bool v1);
+Q8TcKernel q8_tc_d128(int rows, int dtype, bool v1);
+Q8TcKernel q8_tc_d256(int rows, int dtype, bool v1);
 
-inline Q8TcKernel q8_tc(int head_dim, int rows, int dtype)
+inline Q8TcKernel q8_tc(int head_dim, int rows, int dtype, bool v1)
 {
-    return head_dim == 64    ? q8_tc_d64(rows, dtype)
-           : head_dim == 128 ? q8_tc_d128(rows, dtype)
-                             : q8_tc_d256(rows, dtype);
+    return head_dim == 64    ? q8_tc_d64(rows, dtype, v1)
+           : head_dim == 128 ? q8_tc_d128(rows, dtype, v1)
+                             : q8_tc_d256(rows, dtype, v1);
 }
 
 } // namespace pa

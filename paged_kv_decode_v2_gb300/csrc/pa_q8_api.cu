@@ -2,6 +2,7 @@
 // include/pa_decode.h: appending to a paged cache (16-bit or 8-bit) and
 // attention over an 8-bit cache.  Host-side validation, TMA descriptors,
 // launch sizing and dispatch.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -25,17 +26,17 @@ int rows_per_cta(int cols, int head_dim)
     return cols <= 32 || head_dim == 256 ? 32 : 64;
 }
 
-std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2];
+std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
 
-int launch_tc(Q8Launch &L, int dev, int sms, int nr, cudaStream_t stream, int *ctas)
+int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
 {
-    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype);
+    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype, L.v1);
     if (!k.fn)
         return PA_ERR_UNSUPPORTED;
     const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
     const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
     std::atomic<int> &cell =
-        g_tc_limit[dev][(di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)];
+        g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
     // Dynamic limit after the opt-in in the low 18 bits, static bytes above them.
     int have = cell.load(std::memory_order_acquire);
     if (have == 0) {
@@ -58,17 +59,12 @@ int launch_tc(Q8Launch &L, int dev, int sms, int nr, cudaStream_t stream, int *c
     // As many CTAs per SM as the kernel is made for, if rings of two stages fit.
     const size_t sm = limit + fixed_static + 1024; // a CTA also takes 1 KB for the system
     size_t per_cta = limit;
-    int per_sm = 1;
     for (int n = k.ctas; n > 1; --n) {
         if (k.fixed_bytes + 4 * tile + fixed_static + 1024 <= sm / n) {
             per_cta = sm / n - 1024 - fixed_static;
-            per_sm = n;
             break;
         }
     }
-    if (L.p.stream)
-        L.grid = dim3((unsigned)(per_sm * sms));
-    *ctas = per_sm * sms;
     int ks = 1, vs = 1;
     while (k.fixed_bytes + (ks + vs + 1) * tile <= per_cta && ks + vs < 2 * kMaxStages) {
         if (ks > vs)
@@ -97,11 +93,15 @@ int launch_tc(Q8Launch &L, int dev, int sms, int nr, cudaStream_t stream, int *c
     cfg.blockDim = dim3(k.threads);
     cfg.dynamicSmemBytes = L.smem_bytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)L.p.ways;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = L.v1 && L.p.ways > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, k.fn, args) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -242,29 +242,55 @@ int row_groups(int cols, int head_dim)
     return (cols + nr - 1) / nr;
 }
 
-// Whether the work is cut into equal stretches (else one CTA per group), and the
-// tiles q_min a stretch has at least, so that a group's partials, at most (n - 1) / q
-// + 2 for its n tiles, fit the np the intermediates have room for.
-bool choose_stream(int num_seqs, long long groups, int cap, int np, int sms, int *q_min)
+// How a call is cut: V2 at `part` tokens, or V1 (part 0) with a cluster of `ways` CTAs
+// per group (sequence, KV head, row tile), `per` tokens each.
+struct Q8Cut {
+    int part, ways, per;
+};
+
+// A CTA costs some 5 us beside its tiles, so partitions are long: as many per group
+// as make one wave of CTAs, where that takes at most kWavePart tokens each (one
+// sequence of 100,000 tokens, 4 KV heads: 1408 tokens 21.4 us, 2048 22.7, 1024 27.2);
+// else kMaxPart if those are three waves or more, so that lengths even out, else
+// kWavePart (64 sequences of up to 32,768: 4096 89 us, 2048 100, 8192 95; 32 of up
+// to 8192: 2048 56 us, 1024 60, 4096 62).
+constexpr int kWavePart = 2048, kMaxPart = 4096;
+// V1 unless a CTA of its cluster has more tiles than a partition by more than this:
+// what the second launch costs (8 groups of 8000 tokens: V2 10.5 us at 4 tiles, V1
+// 12.9 at 8; of 4000 tokens both 4 tiles, 9.9 us in either).
+constexpr int kJoinTiles = 2;
+
+Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_dim, int max_seq_len,
+                 int partition_size, int sms)
 {
-    const long long n = ((long long)cap + kQ8Tok - 1) / kQ8Tok;
-    // A single partial, or two on a grid that leaves every SM at most one CTA: the
-    // merge's launch would cost more than splitting gains.
-    if (np <= 1 || (np == 2 && groups <= sms) || num_seqs > kQ8Seqs || n * groups > INT32_MAX)
-        return false;
-    *q_min = (int)((n - 1) / (np - 1)) + 1;
-    return true;
+    const int nr = rows_per_cta(q_len * group, head_dim);
+    const long long groups = (long long)num_seqs * num_kv_heads * row_groups(q_len * group, head_dim);
+    const long long tiles = ((long long)max_seq_len + kQ8Tok - 1) / kQ8Tok;
+    const long long slots = (long long)sms * (nr <= 32 && head_dim <= 128 ? 2 : 1);
+    Q8Cut cut = {0, 1, 0};
+    if (tiles <= 1)
+        return cut;
+    const long long ways = std::max(1LL, std::min(std::min((long long)kQ8Ways, tiles), sms / groups));
+    const long long per = (tiles + ways - 1) / ways;
+    cut.ways = (int)((tiles + per - 1) / per);
+    cut.per = (int)std::min(per * kQ8Tok, (long long)INT32_MAX);
+    const long long wave = std::max(1LL, slots / groups); // partitions per group in one wave
+    long long part = (tiles + wave - 1) / wave * kQ8Tok;
+    if (part > kWavePart) {
+        const long long np = ((long long)max_seq_len + kMaxPart - 1) / kMaxPart;
+        part = groups * np >= 3 * slots ? kMaxPart : kWavePart;
+    }
+    part = std::max(part, (long long)partition_size);
+    if (part < max_seq_len && per > (part + kQ8Tok - 1) / kQ8Tok + kJoinTiles)
+        cut.part = (int)part;
+    return cut;
 }
 
 // ---- the 16-bit copy for many rows
 
 // From this many query rows per KV head on, the call makes a 16-bit copy of its
 // blocks and runs the 16-bit kernels over it.
-#ifndef Q8CR
-#define Q8CR 256
-#endif
-int copy_rows_default = Q8CR;
-#define kQ8CopyRows copy_rows_default
+constexpr int kQ8CopyRows = 256;
 
 struct CopyPlan {
     bool v_half;   // V in binary16 beside a bf16 K, for the two-tile kernel
@@ -324,6 +350,15 @@ bool plan_copy(CopyPlan &plan, Q8CopyParams &c, const Q8Params &p, int partition
     return true;
 }
 
+int check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                 int max_seq_len, int partition_size)
+{
+    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -364,6 +399,19 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
                        (cudaStream_t)stream);
 }
 
+PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                  int head_dim, int max_seq_len, int partition_size)
+{
+    if (check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len, partition_size))
+        return -PA_ERR_INVALID_ARG;
+    int dev, sms;
+    if (host_device(&dev, &sms))
+        return -PA_ERR_CUDA;
+    return choose_cut(num_seqs, q_len, num_heads / num_kv_heads, num_kv_heads, head_dim, max_seq_len,
+                      partition_size, sms)
+        .part;
+}
+
 PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *value_cache,
                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
                         const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,
@@ -397,14 +445,13 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     const bool work_ok = tmp_output && exp_sums && max_logits && max_num_partitions > 0 &&
                          host_aligned(tmp_output, 16) && host_aligned(exp_sums, 4) &&
                          host_aligned(max_logits, 4);
-    const int np = pa_v2_num_partitions(cap, partition_size);
-    const int col_groups = row_groups(group * q_len, head_dim);
-    int q_min = 1;
-    const bool streamed =
-        choose_stream(num_seqs, (long long)num_seqs * num_kv_heads * col_groups, cap, np, sms, &q_min);
-    if (streamed && !work_ok)
+    const Q8Cut cut =
+        choose_cut(num_seqs, q_len, group, num_kv_heads, head_dim, cap, partition_size, sms);
+    const int part = cut.part;
+    const int np = part ? pa_v2_num_partitions(cap, part) : 1;
+    if (part && !work_ok)
         return PA_ERR_INVALID_ARG;
-    if (streamed && np > max_num_partitions)
+    if (part && np > max_num_partitions)
         return PA_ERR_WORKSPACE;
 
     Q8Launch L = {};
@@ -426,15 +473,14 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.group = group;
     p.q_len = q_len;
     p.cols = group * q_len;
-    p.col_groups = col_groups;
+    p.col_groups = row_groups(p.cols, head_dim);
     p.num_blocks = num_blocks;
     p.block_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
     p.max_blocks = max_blocks_per_seq;
     p.seq_len_cap = cap;
     p.scale = scale;
-    p.stream = streamed;
-    p.num_seqs = num_seqs;
-    p.q_min = q_min;
+    p.partition_size = part ? part : cut.per;
+    p.ways = cut.ways;
     p.max_num_partitions = max_num_partitions;
     p.tmp_output = tmp_output;
     p.exp_sums = exp_sums;
@@ -443,6 +489,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.status = status;
     L.head_dim = head_dim;
     L.block_size = block_size;
+    L.v1 = part == 0;
 
     if (work_ok && p.cols >= kQ8CopyRows) {
         Q8CopyParams c = {};
@@ -458,22 +505,23 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
                                    plan.np, dtype, out, tmp_output, exp_sums, max_logits, status, st);
             if (rc || !plan.may_flag)
                 return rc;
-            // Values that binary16 cannot hold: the 8-bit kernel runs after all (a CTA
-            // per group, which needs no intermediates, over the result above).
+            // Values that binary16 cannot hold: the 8-bit kernel runs after all (V1,
+            // which needs no intermediates, over the result above).
             p.only_if = c.flag;
-            p.stream = 0;
+            L.v1 = true;
+            p.ways = 1;
         }
     }
-    // Row tiles of one KV head are neighbours: their reads meet in L2.
-    L.grid = dim3(col_groups, num_kv_heads, num_seqs);
-    int ctas = 0;
-    rc = launch_tc(L, dev, sms, rows_per_cta(p.cols, head_dim), st, &ctas);
-    if (rc || !p.stream)
+    // Column groups of one partition are adjacent in x: their reads meet in L2.
+    const long long gx = (long long)(L.v1 ? p.ways : np) * p.col_groups;
+    if (gx > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
+    rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);
+    if (rc || L.v1)
         return rc;
-    const StreamPlan plan = {num_seqs, num_kv_heads, col_groups, rows_per_cta(p.cols, head_dim),
-                             kQ8Tok,   ctas,         q_min};
-    return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, partition_size, dtype,
-                      tmp_output, exp_sums, max_logits, max_num_partitions, out, plan, status, st);
+    return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
+                      exp_sums, max_logits, max_num_partitions, out, status, st);
 }
 
 } // extern "C"

@@ -58,9 +58,6 @@
 
 namespace pa {
 
-#ifndef Q8_MC
-#define Q8_MC 2
-#endif
 constexpr float kQ8Ln2 = 0.69314718055994531f;
 constexpr float kQ8NoMax = -1e30f; // M before a row has seen a token
 constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4,
@@ -199,6 +196,33 @@ __device__ __forceinline__ bool bar_any(int id, int count, bool v)
     return r != 0;
 }
 
+// ---- thread-block clusters: all threads of all CTAs meet; a peer's shared memory
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // An int whose order is the float's (no NaN), and back.
 __device__ __forceinline__ int ordered(float x)
 {
@@ -218,6 +242,48 @@ __device__ __forceinline__ void q_row_scale(float amax, float &f, float &inv)
     const int fe = amax > 0.f ? min(127 + 7 - (e - 127), 253) : 127;
     f = __uint_as_float((uint32_t)fe << 23);
     inv = __uint_as_float((uint32_t)(254 - fe) << 23);
+}
+
+// V1 over a cluster: the CTAs' partials of the same rows (o normalised, l, M in log2
+// units; M = -inf, l = 0 without a token) -> out.  `o_sm` [NR][D] and `ml` [2][NR] in
+// every CTA's shared memory; each CTA joins every ways-th four values.  All threads
+// of the CTA call it, its partial written and synchronised.
+template <int D, int NR, typename T, typename RowOf>
+__device__ __forceinline__ void join_cluster(uint32_t o_sm, uint32_t ml, int rank, int ways, int nrows,
+                                             T *out, RowOf row_of)
+{
+    using E = Elem<T>;
+    cluster_sync();
+    for (int i = threadIdx.x * ways + rank; i < nrows * (D / 4); i += blockDim.x * ways) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float m[kQ8Ways], l[kQ8Ways], top = -INFINITY;
+        float4 o[kQ8Ways];
+#pragma unroll
+        for (int w = 0; w < kQ8Ways; ++w) {
+            const int from = w < ways ? w : rank;
+            m[w] = ld_peer(peer_addr(ml + 4 * r, from));
+            l[w] = w < ways ? ld_peer(peer_addr(ml + 4 * (NR + r), from)) : 0.f;
+            o[w] = ld_peer4(peer_addr(o_sm + (r * D + d) * 4, from));
+            top = fmaxf(top, m[w]);
+        }
+        float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kQ8Ways; ++w) {
+            if (l[w] > 0.f) { // (an empty one's o may be anything)
+                const float f = l[w] * fast_exp2(m[w] - top);
+                sum += f;
+                x[0] += f * o[w].x;
+                x[1] += f * o[w].y;
+                x[2] += f * o[w].z;
+                x[3] += f * o[w].w;
+            }
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        uint32_t *const dst = reinterpret_cast<uint32_t *>(out + row_of(r) * D + d);
+        dst[0] = E::pack(x[0] * inv, x[1] * inv);
+        dst[1] = E::pack(x[2] * inv, x[3] * inv);
+    }
+    cluster_sync(); // the peers have read this CTA's part
 }
 
 // ---------------------------------------------------------------- shape
@@ -249,26 +315,12 @@ struct Q8Cfg {
     static_assert(kWG * 128 <= kQ8Chap, "a thread holds one block of the first chapter");
     static constexpr int kSoft = kWG * 128;
     static constexpr int kThreads = kSoft + 64 + 32 * kQ8Load;
-    static constexpr int kMinCtas = D > 128 ? 1 : NR <= 8 ? Q8_MC : NR <= 32 ? 2 : 1;
+    static constexpr int kMinCtas = D > 128 ? 1 : NR <= 32 ? 2 : 1;
     static constexpr int kCtas = kMinCtas * (int)kCols <= 512 ? kMinCtas : 512 / (int)kCols;
     static constexpr uint32_t kFixed = 1024 + kBuf * kPBytes + kQBytes;
 };
 
-// One stretch of work of a CTA: tiles [t_lo, t_hi) of sequence b for KV head kv
-// and row tile rt.
-struct Q8Seg {
-    int b, kv, rt, t_lo, t_hi;
-    int part;    // index among the group's partials
-    bool whole;  // all of the group's tiles: the output itself
-    int len;     // the sequence's length, clamped
-};
-
-// Work is the groups (sequence, KV head, row tile) one after another, sequences
-// outermost, each of as many 128-token tiles as its sequence has.  p.stream: CTA c
-// takes tiles [c q, (c + 1) q) of that order, q = max(ceil(total / CTAs), q_min),
-// so that all CTAs read alike whatever the lengths; a group cut between CTAs
-// leaves partials, numbered by CTA.  Otherwise one CTA per group.
-template <int D, int NR, int PL>
+template <int D, int NR, int PL, bool V1>
 __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::kMinCtas)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
@@ -281,7 +333,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
 
     __shared__ uint64_t k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages],
         v_empty[kMaxStages];
-    __shared__ uint64_t s_full[2], p_full[2], o_done[2], q_full, drained[2];
+    __shared__ uint64_t s_full[2], p_full[2], o_done[2], drained[2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     __shared__ __align__(16) float s_cf[NR];   // a row's raw products -> log2 units (but for ks)
@@ -289,16 +341,23 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     __shared__ float s_al[NR];                 // 2^(M_old - M_new)
     __shared__ float s_inv[NR];                // r / l
     __shared__ size_t s_row[NR];               // rows of out, or slots of the intermediates
+    __shared__ float s_ml[2 * NR];             // a cluster's join: M and l
     __shared__ int s_red[C::kSoft / 32][kRW];
     __shared__ float s_part[C::kSoft / 32][kRW];
     __shared__ float s_vref[C::kSoft / 32];
     __shared__ float s_ks[kQ8Chap], s_lv[kQ8Chap], s_rl[kQ8Chap]; // a chapter's ks, lv, 2^-lv
-    __shared__ int s_base[kQ8Seqs + 1];        // tiles of the sequences before each one
-    __shared__ int s_len[kQ8Seqs];
     extern __shared__ uint8_t dyn_smem[];
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    // blockIdx.x = partition * col_groups + row tile; V1: row tile * ways + rank, the
+    // `ways` CTAs of a cluster a row tile's partitions.
+    const bool one_group = p.col_groups == 1;
+    const int ways = V1 ? p.ways : 1;
+    const int rt = V1 ? (int)blockIdx.x / ways : one_group ? 0 : (int)blockIdx.x % p.col_groups;
+    const int part = V1 ? (int)blockIdx.x % ways : one_group ? (int)blockIdx.x : (int)blockIdx.x / p.col_groups;
+    const int kv = blockIdx.y;
+    const int b = blockIdx.z;
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmap_k);
@@ -311,135 +370,74 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     if (p.only_if && __ldcg(p.only_if) == 0)
         return;
 
+    const int tokA = part * p.partition_size;
     const int sh = p.block_shift, bs = 1 << sh; // block size
     const int bpt = kQ8Tok >> sh;               // blocks per tile: 2 to 16
-    const int kr = p.num_kv_heads * p.col_groups;
-    auto length = [&](int b, bool report) -> int {
-        const int L = __ldg(p.seq_lens + b);
-        if (L >= 0 && L <= p.seq_len_cap)
-            return L;
-        if (report)
+    const int blk0 = tokA >> sh;
+    const int32_t *bt = p.block_tables + (size_t)b * p.max_blocks + blk0;
+    // The table's first entries, loaded beside the length.
+    int32_t id_first = 0;
+    if (threadIdx.x < C::kSoft && blk0 + (int)threadIdx.x < p.max_blocks)
+        id_first = __ldg(bt + threadIdx.x);
+    int L = __ldg(&p.seq_lens[b]);
+    if (L < 0 || L > p.seq_len_cap) {
+        if (threadIdx.x == 0 && part == 0 && kv == 0 && rt == 0)
             set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
-        return L < 0 ? 0 : p.seq_len_cap;
-    };
-    auto tiles_of = [](int L) -> int { return (int)(((long long)L + kQ8Tok - 1) / kQ8Tok); };
-
-    // ---- this CTA's stretch of the order
-    int w = 0, w_end = 0, per_cta = 1; // position, end, q
-    Q8Seg first;
-    if (p.stream) {
-        for (int b = threadIdx.x; b < p.num_seqs; b += C::kThreads) {
-            const int L = length(b, blockIdx.x == 0);
-            s_len[b] = L;
-            s_base[b + 1] = tiles_of(L);
-        }
-        if (threadIdx.x == 0)
-            s_base[0] = 0;
-        __syncthreads();
-        if (warp == 0) {
-            // Inclusive scan: each lane a run of sequences, then the lanes.
-            const int per = (p.num_seqs + 31) / 32;
-            const int b0 = lane * per, b1 = min(b0 + per, p.num_seqs);
-            int sum = 0;
-            for (int b = b0; b < b1; ++b)
-                sum += s_base[b + 1];
-            int run = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, run, off);
-                run += lane >= off ? v : 0;
-            }
-            run -= sum;
-            for (int b = b0; b < b1; ++b) {
-                run += s_base[b + 1];
-                s_base[b + 1] = run;
-            }
-        }
-        __syncthreads();
-        const int total = s_base[p.num_seqs] * kr;
-        per_cta = max((total + (int)gridDim.x - 1) / (int)gridDim.x, p.q_min);
-        const long long at = (long long)blockIdx.x * per_cta;
-        if (at >= total)
-            return;
-        w = (int)at;
-        w_end = min(w + per_cta, total);
-        int lo = 0, hi = p.num_seqs - 1; // the last b that starts at or before w
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_base[mid] * kr <= w)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        first.b = lo;
-    } else {
-        first.b = blockIdx.z;
-        first.kv = blockIdx.y;
-        first.rt = blockIdx.x;
-        first.len = length(first.b, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
-        first.t_lo = 0;
-        first.t_hi = tiles_of(first.len);
-        first.part = 0;
-        first.whole = true;
-        w_end = 1;
+        L = L < 0 ? 0 : p.seq_len_cap;
     }
-    // The stretch at position w (its sequence known), and the step past it.
-    auto at_work = [&](Q8Seg &sg, int pos) {
-        if (!p.stream)
-            return;
-        const int n = s_base[sg.b + 1] - s_base[sg.b];
-        const int local = pos - s_base[sg.b] * kr;
-        const int group = local / n;
-        sg.t_lo = local - group * n;
-        sg.t_hi = min(n, sg.t_lo + (w_end - pos));
-        sg.kv = p.col_groups == 1 ? group : group / p.col_groups;
-        sg.rt = p.col_groups == 1 ? 0 : group % p.col_groups;
-        sg.whole = sg.t_lo == 0 && sg.t_hi == n;
-        sg.part = (int)blockIdx.x - (pos - sg.t_lo) / per_cta;
-        sg.len = s_len[sg.b];
-    };
-    auto advance = [&](Q8Seg &sg, int &pos) { // to the next stretch; pos == w_end after the last
-        if (!p.stream) {
-            pos = w_end;
-            return;
-        }
-        pos += sg.t_hi - sg.t_lo;
-        if (pos < w_end) {
-            while (s_base[sg.b + 1] * kr <= pos)
-                ++sg.b;
-            at_work(sg, pos);
-        }
-    };
-    at_work(first, w);
+    if (!V1 && tokA >= L)
+        return; // partition past the end of the sequence: nothing to write
 
-    // What a stretch means for the rows [c0, c0 + nrows) of the KV head's cols =
-    // q_len * group rows, and for the tokens [tok0, tok_e): up to the causal limit of
+    // Rows [c0, c0 + nrows) of the KV head's cols = q_len * group rows.
+    const int c0 = rt * NR;
+    const int nrows = min(NR, p.cols - c0);
+    const int i_last = p.q_len == 1 ? 0 : (c0 + nrows - 1) / p.group;
+    auto row_of = [&](int r) -> size_t { // row of [S * q_len * H] of local row r
+        const int c = c0 + r;
+        if (p.q_len == 1)
+            return (size_t)b * p.num_heads + kv * p.group + c;
+        return ((size_t)b * p.q_len + c / p.group) * p.num_heads + kv * p.group + c % p.group;
+    };
+    // Tokens the CTA needs: [tokA, tokE), the range cut by the causal limit of
     // its last new token (new token i sees positions <= L - q_len + i).
-    struct Range {
-        int c0, nrows, tok0, tok_e, ntiles, nblk;
-    };
-    auto range_of = [&](const Q8Seg &sg) -> Range {
-        Range r;
-        r.c0 = sg.rt * NR;
-        r.nrows = min(NR, p.cols - r.c0);
-        const int i_last = p.q_len == 1 ? 0 : (r.c0 + r.nrows - 1) / p.group;
-        r.tok0 = sg.t_lo * kQ8Tok;
-        const long long e = min(min((long long)sg.len, (long long)sg.t_hi * kQ8Tok),
-                                (long long)sg.len - p.q_len + i_last + 1);
-        r.tok_e = (int)max(e, (long long)r.tok0);
-        r.ntiles = tiles_of(r.tok_e - r.tok0);
-        r.nblk = (int)(((long long)r.tok_e - r.tok0 + bs - 1) >> sh);
-        return r;
-    };
-    auto table_of = [&](const Q8Seg &sg, const Range &r) -> const int32_t * {
-        return p.block_tables + (size_t)sg.b * p.max_blocks + (r.tok0 >> sh);
-    };
-    // A block's id, or 0 (a valid block) when out of range.
-    auto valid_id = [&](int32_t id) -> int32_t { return id < 0 || id >= p.num_blocks ? 0 : id; };
+    long long e = ways == 1 && V1 ? (long long)L : min((long long)L, (long long)tokA + p.partition_size);
+    e = min(e, (long long)L - p.q_len + i_last + 1);
+    const int tokE = (int)e;
+    const int tok0 = blk0 << sh;
+    const int ntiles = tokE > tokA ? (tokE - tok0 + kQ8Tok - 1) / kQ8Tok : 0;
+    const int nblk = tokE > tokA ? (tokE - tok0 + bs - 1) >> sh : 0;
+
+    const uint32_t smem0 = (smem_addr(dyn_smem) + 1023u) & ~1023u;
+    if (ntiles == 0) {
+        // No row sees a token of the range: an empty partition (m = -inf,
+        // l = 0, o = 0), or a zero output in V1.
+        if (V1 && ways > 1) {
+            if (threadIdx.x < NR) {
+                s_ml[threadIdx.x] = -INFINITY;
+                s_ml[NR + threadIdx.x] = 0.f;
+            }
+            __syncthreads();
+            join_cluster<D, NR>(smem0, smem_addr(s_ml), part, ways, nrows, static_cast<T *>(p.out), row_of);
+            return;
+        }
+        for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
+            const size_t row = row_of(idx / D);
+            if (V1) {
+                static_cast<T *>(p.out)[row * D + idx % D] = E::from_float(0.f);
+            } else {
+                const size_t slot = row * p.max_num_partitions + part;
+                p.tmp_output[slot * D + idx % D] = 0.f;
+                if (idx % D == 0) {
+                    p.exp_sums[slot] = 0.f;
+                    p.max_logits[slot] = -INFINITY;
+                }
+            }
+        }
+        return;
+    }
 
     const int kst = p.stages;   // K ring stages
     const int vst = p.v_stages; // V ring stages
-    const uint32_t smem0 = (smem_addr(dyn_smem) + 1023u) & ~1023u;
     const uint32_t k_sm = smem0;
     const uint32_t v_sm = k_sm + (uint32_t)kst * C::kTile;
     const uint32_t p_sm = v_sm + (uint32_t)vst * C::kTile;
@@ -447,15 +445,49 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     const uint32_t b_k_full = smem_addr(k_full), b_v_full = smem_addr(v_full);
     const uint32_t b_k_empty = smem_addr(k_empty), b_v_empty = smem_addr(v_empty);
     const uint32_t b_s_full = smem_addr(s_full), b_p_full = smem_addr(p_full);
-    const uint32_t b_o_done = smem_addr(o_done), b_q_full = smem_addr(&q_full);
-    const uint32_t b_drained = smem_addr(drained);
+    const uint32_t b_o_done = smem_addr(o_done), b_drained = smem_addr(drained);
     volatile int *abort_flag = &abort_sh;
-    int32_t status_bits = 0;
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(&tmem_base_sh), C::kCols);
         tmem_relinquish();
     }
+    int32_t status_bits = 0;
+    // Producer warp w loads half w & 1 of the blocks of every K (w < 2) or V tile.
+    // One warp issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80
+    // clocks each) would bound the loop.
+    const int pw = warp - kTmaWarp;
+    const bool is_k = pw < 2;
+    const int p_first = (pw & 1) * (bpt / 2), p_num = bpt / 2; // its blocks of a tile
+    const int p_stages = is_k ? kst : vst;
+    const uint32_t p_full_bar = is_k ? b_k_full : b_v_full, p_empty_bar = is_k ? b_k_empty : b_v_empty;
+    const uint32_t p_ring = is_k ? k_sm : v_sm;
+    const CUtensorMap *p_map = is_k ? &tmap_k : &tmap_v;
+    const uint64_t policy = p.col_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
+    auto fetch_id = [&](int t) -> int32_t { // this lane's block of tile t
+        const int i = t * bpt + p_first + lane;
+        return lane < p_num && i < nblk ? __ldg(bt + i) : 0;
+    };
+    auto load_tile = [&](int s, int t, int32_t id) {
+        const int nb = min(max(nblk - t * bpt - p_first, 0), p_num);
+        if (id < 0 || id >= p.num_blocks) {
+            status_bits |= PA_STATUS_BAD_BLOCK_ID;
+            id = 0; // read a valid block instead of memory outside the cache
+        }
+        const uint32_t bar = p_full_bar + 8 * s;
+        const uint32_t dst = p_ring + (uint32_t)s * C::kTile + p_first * bs * C::kRB;
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, (uint32_t)nb * bs * D);
+        for (int i = 0; i < nb; ++i) {
+            const int32_t phys = __shfl_sync(0xffffffffu, id, i);
+            if (lane == 0) {
+                const int row = (int)(((long long)phys * p.num_kv_heads + kv) * bs);
+#pragma unroll
+                for (int sl = 0; sl < C::kSlices; ++sl)
+                    tma_load_3d(dst + sl * C::kSlice + i * bs * C::kRB, p_map, 0, sl, row, bar, policy);
+            }
+        }
+    };
     if (threadIdx.x == kTmaWarp * 32) {
         for (int s = 0; s < kst; ++s) {
             mbar_init(b_k_full + 8 * s, 2);
@@ -470,81 +502,94 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
             mbar_init(b_p_full + 8 * j, C::kSoft);
             mbar_init(b_o_done + 8 * j, 1);
         }
-        mbar_init(b_q_full, C::kSoft);
         mbar_init(b_drained, 1);
         mbar_init(b_drained + 8, 1);
         abort_sh = 0;
         mbar_init_fence();
     }
-
-    // ---- producers' state.  Producer warp w loads half w & 1 of the blocks of every
-    // K (w < 2) or V tile: one warp issuing all of a tile's TMA loads (16 at 16-token
-    // blocks, 40-80 clocks each) would bound the loop.
-    const int pw = warp - kTmaWarp;
-    const bool is_k = pw < 2;
-    const int p_first = (pw & 1) * (bpt / 2), p_num = bpt / 2; // its blocks of a tile
-    const int p_stages = is_k ? kst : vst;
-    const uint32_t p_full_bar = is_k ? b_k_full : b_v_full, p_empty_bar = is_k ? b_k_empty : b_v_empty;
-    const uint32_t p_ring = is_k ? k_sm : v_sm;
-    const CUtensorMap *p_map = is_k ? &tmap_k : &tmap_v;
-    const uint64_t policy = p.col_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
-    Q8Seg p_seg = first;
-    int p_pos = w, p_tile = 0, p_stage = 0;
-    uint32_t p_phase = 0u, issued = 0u;
-    Range p_rg = range_of(p_seg);
-    const int32_t *p_bt = table_of(p_seg, p_rg);
-    int32_t id_next = 0; // this lane's block of the next tile, fetched ahead of its stage
-    auto fetch_id = [&](int t) -> int32_t {
-        const int i = t * bpt + p_first + lane;
-        return lane < p_num && i < p_rg.nblk ? __ldg(p_bt + i) : 0;
-    };
-    // Moves to a stretch with tiles left; false after the last.
-    auto p_more = [&]() -> bool {
-        while (p_tile == p_rg.ntiles) {
-            advance(p_seg, p_pos);
-            if (p_pos >= w_end)
-                return false;
-            p_rg = range_of(p_seg);
-            p_bt = table_of(p_seg, p_rg);
-            p_tile = 0;
-            id_next = fetch_id(0);
-        }
-        return true;
-    };
-    auto load_tile = [&]() {
-        const int nb = min(max(p_rg.nblk - p_tile * bpt - p_first, 0), p_num);
-        int32_t id = id_next;
-        id_next = fetch_id(p_tile + 1);
-        if (id < 0 || id >= p.num_blocks) {
-            status_bits |= PA_STATUS_BAD_BLOCK_ID;
-            id = 0; // read a valid block instead of memory outside the cache
-        }
-        const uint32_t bar = p_full_bar + 8 * p_stage;
-        const uint32_t dst = p_ring + (uint32_t)p_stage * C::kTile + p_first * bs * C::kRB;
-        if (lane == 0)
-            mbar_arrive_expect_tx(bar, (uint32_t)nb * bs * D);
-        for (int i = 0; i < nb; ++i) {
-            const int32_t phys = __shfl_sync(0xffffffffu, id, i);
-            if (lane == 0) {
-                const int row = (int)(((long long)phys * p.num_kv_heads + p_seg.kv) * bs);
-#pragma unroll
-                for (int sl = 0; sl < C::kSlices; ++sl)
-                    tma_load_3d(dst + sl * C::kSlice + i * bs * C::kRB, p_map, 0, sl, row, bar, policy);
-            }
-        }
-        ++p_tile;
-        ++issued;
-        if (++p_stage == p_stages) {
-            p_stage = 0;
-            p_phase ^= 1u;
-        }
-    };
+    int issued = 0;          // tiles this producer has issued
+    int32_t id_next = 0;     // this lane's block of the next one, fetched ahead of its stage
     if (warp >= kTmaWarp) {
         // The first tiles, before the rest of the set-up.
         bar_sync(15, 32 * kQ8Load); // the barriers are initialised
         id_next = fetch_id(0);
-        while ((int)issued < p_stages && p_more())
-            load_tile();
+        while (issued < ntiles && issued < p_stages) {
+            const int32_t id = id_next;
+            id_next = fetch_id(issued + 1);
+            load_tile(issued, issued, id);
+            ++issued;
+        }
+    }
+    // A block's id, or 0 (a valid block) when out of range.
+    auto valid_id = [&](int32_t id) -> int32_t { return id < 0 || id >= p.num_blocks ? 0 : id; };
+
+    float vref = 1.1754943508222875e-38f; // 2^-126, or the range's largest V scale
+    float ks_first = 0.f, vs_first = 0.f; // scales of block threadIdx.x
+    if (warp < kMmaWarp) {
+        // Q rows -> shared memory in PL parts, K-major, swizzled (16-byte chunk c of
+        // row n at c ^ (n & 7), of 64-byte rows c ^ (n >> 1 & 3)); a warp per row.
+        constexpr int kDL = D / 32;                 // consecutive dims of a lane: 2, 4 or 8
+        constexpr int kRows = NR / (C::kSoft / 32); // rows of a warp
+        uint32_t q_raw[kRows][kDL / 2];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = warp + i * (C::kSoft / 32);
+            const uint32_t *q32 = static_cast<const uint32_t *>(p.query) +
+                                  row_of(r < nrows ? r : 0) * (D / 2) + lane * (kDL / 2);
+#pragma unroll
+            for (int k = 0; k < kDL / 2; ++k)
+                q_raw[i][k] = r < nrows ? __ldg(q32 + k) : 0u;
+        }
+        if ((int)threadIdx.x < nblk) {
+            const size_t at = (size_t)valid_id(id_first) * p.num_kv_heads + kv;
+            ks_first = __ldg(p.k_scales + at);
+            vs_first = __ldg(p.v_scales + at);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = warp + i * (C::kSoft / 32);
+            float x[kDL], m = 0.f;
+#pragma unroll
+            for (int k = 0; k < kDL / 2; ++k) {
+                x[2 * k] = E::lo(q_raw[i][k]);
+                x[2 * k + 1] = E::hi(q_raw[i][k]);
+                m = fmaxf(m, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            float f, inv;
+            q_row_scale(m, f, inv);
+            if (lane == 0) {
+                s_cf[r] = p.scale * inv * kLog2e;
+                s_nm[r] = -kQ8NoMax;
+                const size_t row = row_of(r < nrows ? r : 0);
+                s_row[r] = V1 ? row : row * p.max_num_partitions + part;
+            }
+#pragma unroll
+            for (int k = 0; k < kDL; ++k) // a value that is not finite becomes NaN
+                x[k] = fabsf(x[k]) <= 3.4028234663852886e38f ? x[k] * f : NAN;
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                const int n = k * NR + r;
+                const int d = lane * kDL;          // first dim
+                const int c = (d % C::kRB) >> 4;   // 16-byte chunk
+                const int sw = C::kRB == 128 ? c ^ (n & 7) : c ^ ((n >> 1) & 3);
+                const uint32_t dst = q_sm + (d / C::kRB) * (C::kSN * C::kRB) + n * C::kRB +
+                                     (sw << 4) + (d & 15);
+#pragma unroll
+                for (int h = 0; h < kDL / 2; ++h) {
+                    const uint32_t code = __nv_cvt_float2_to_fp8x2(
+                        make_float2(x[2 * h], x[2 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * h), "h"((unsigned short)code)
+                                 : "memory");
+                    const uint32_t back = e4m3_to_f16(code);
+                    x[2 * h] = (x[2 * h] - Elem<__half>::lo(back)) * 16.f;
+                    x[2 * h + 1] = (x[2 * h + 1] - Elem<__half>::hi(back)) * 16.f;
+                }
+            }
+        }
+        fence_proxy_async();
     }
     tc_fence_before();
     __syncthreads();
@@ -553,20 +598,25 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
 
     if (warp >= kTmaWarp) {
         // ---------------------------------------------------------- producers
-        while (p_more()) {
-            // (the phase flipped when the ring went round: the fill before is ph ^ 1)
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait_abortable(p_empty_bar + 8 * p_stage, p_phase ^ 1u, abort_flag))) {
+        int s = 0;
+        uint32_t ph = 0u;
+        for (; issued < ntiles; ++issued) {
+            if (!__all_sync(0xffffffffu, mbar_wait_abortable(p_empty_bar + 8 * s, ph, abort_flag))) {
                 status_bits |= PA_STATUS_TIMEOUT;
                 *abort_flag = 1;
                 break;
             }
-            load_tile();
+            load_tile(s, issued, id_next);
+            id_next = fetch_id(issued + 1);
+            if (++s == p_stages) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
         // Let copies still in flight land before the shared memory is released
         // (normally consumed long ago; bounded).
-        for (uint32_t t = issued > (uint32_t)p_stages ? issued - p_stages : 0u; t < issued; ++t)
-            mbar_wait_bounded(p_full_bar + 8 * (t % p_stages), (t / p_stages) & 1u, kWaitLimitNs);
+        for (int t = max(0, issued - p_stages); t < issued; ++t)
+            mbar_wait_bounded(p_full_bar + 8 * (t % p_stages), (uint32_t)(t / p_stages) & 1u, kWaitLimitNs);
         __syncwarp();
     } else if (warp >= kMmaWarp) {
         // ---------------------------------------------------------- MMA issuers
@@ -584,81 +634,67 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         const uint64_t vd = smem_desc_sw<C::kRB>(v_sm, 8 * C::kRB, 8 * C::kRB);
         const uint64_t pd = smem_desc_sw<C::kPW>(p_sm, C::kPGroup, 8 * C::kPW);
         bool ok = true;
-        int s = 0;           // ring stage of tile g
-        uint32_t ph = 0u, qph = 0u;
-        int g = 0;           // tiles so far, over all stretches
-        Q8Seg sg = first;
-        for (int pos = w; ok && pos < w_end; advance(sg, pos)) {
-            const Range rg = range_of(sg);
-            if (rg.ntiles == 0)
-                continue;
+        int s = 0; // ring stage of tile t
+        uint32_t ph = 0u;
+        for (int t = 0; t < ntiles; ++t) {
+            const int j = C::kBuf == 2 ? t & 1 : 0;
             if (is_s) {
-                ok = __all_sync(0xffffffffu, mbar_wait_abortable(b_q_full, qph, abort_flag));
-                qph ^= 1u;
-            }
-            for (int t = 0; ok && t < rg.ntiles; ++t, ++g) {
-                const int j = C::kBuf == 2 ? g & 1 : 0;
-                if (is_s) {
-                    // S(g) once its K tile has landed and softmax(g - kBuf) has read the buffer.
-                    ok = mbar_wait_abortable(b_k_full + 8 * s, ph, abort_flag) &&
-                         (g < C::kBuf ||
-                          mbar_wait_abortable(b_p_full + 8 * ((g - C::kBuf) & 1),
-                                              (uint32_t)((g - C::kBuf) >> 1) & 1u, abort_flag));
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        constexpr uint32_t idesc = idesc_f8(128, C::kSN, false, false);
-                        const uint64_t kb = kd + (((uint32_t)s * C::kTile) >> 4);
+                // S(t) once K tile t has landed and softmax(t - kBuf) has read the buffer.
+                ok = mbar_wait_abortable(b_k_full + 8 * s, ph, abort_flag) &&
+                     (t < C::kBuf ||
+                      mbar_wait_abortable(b_p_full + 8 * ((t - C::kBuf) & 1),
+                                          (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag));
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint32_t idesc = idesc_f8(128, C::kSN, false, false);
+                    const uint64_t kb = kd + (((uint32_t)s * C::kTile) >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < D / 32; ++ks) {
-                            constexpr int kPer = C::kRB / 32;
-                            const uint32_t off_k = (ks / kPer) * C::kSlice + (ks % kPer) * 32;
-                            const uint32_t off_q = (ks / kPer) * (C::kSN * C::kRB) + (ks % kPer) * 32;
-                            tc_mma_f8(tmem + C::kSCol + j * C::kSReg, kb + (off_k >> 4),
-                                      qd + (off_q >> 4), idesc, ks > 0);
-                        }
-                        tc_commit(b_s_full + 8 * (g & 1));
-                        tc_commit(b_k_empty + 8 * s);
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        constexpr int kPer = C::kRB / 32;
+                        const uint32_t off_k = (ks / kPer) * C::kSlice + (ks % kPer) * 32;
+                        const uint32_t off_q = (ks / kPer) * (C::kSN * C::kRB) + (ks % kPer) * 32;
+                        tc_mma_f8(tmem + C::kSCol + j * C::kSReg, kb + (off_k >> 4), qd + (off_q >> 4),
+                                  idesc, ks > 0);
                     }
-                    __syncwarp();
-                    if (++s == kst) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                } else {
-                    // P.V(g) once P(g) is written and its V tile has landed.
-                    ok = mbar_wait_abortable(b_v_full + 8 * s, ph, abort_flag) &&
-                         mbar_wait_abortable(b_p_full + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        constexpr uint32_t idesc = idesc_f8(128, C::kPN, true, true);
-                        const uint64_t vb = vd + (((uint32_t)s * C::kTile) >> 4);
-                        const uint64_t pb = pd + ((j * C::kPBytes) >> 4);
+                    tc_commit(b_s_full + 8 * (t & 1));
+                    tc_commit(b_k_empty + 8 * s);
+                }
+                __syncwarp();
+                if (++s == kst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            } else {
+                // P.V(t) once P(t) is written and V tile t has landed.
+                ok = mbar_wait_abortable(b_v_full + 8 * s, ph, abort_flag) &&
+                     mbar_wait_abortable(b_p_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint32_t idesc = idesc_f8(128, C::kPN, true, true);
+                    const uint64_t vb = vd + (((uint32_t)s * C::kTile) >> 4);
+                    const uint64_t pb = pd + ((j * C::kPBytes) >> 4);
 #pragma unroll
-                        for (int h = 0; h < C::kMB; ++h)
+                    for (int h = 0; h < C::kMB; ++h)
 #pragma unroll
-                            for (int kt = 0; kt < kQ8Tok / 32; ++kt)
-                                tc_mma_f8(tmem + h * C::kOReg,
-                                          vb + ((h * C::kSlice + kt * 32 * C::kRB) >> 4),
-                                          pb + ((kt * 32 * C::kPW) >> 4), idesc,
-                                          kt > 0 ? 1u : (t > 0 ? 1u : 0u));
-                        tc_commit(b_o_done + 8 * (g & 1));
-                        tc_commit(b_v_empty + 8 * s);
-                    }
-                    __syncwarp();
-                    if (++s == vst) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                        for (int kt = 0; kt < kQ8Tok / 32; ++kt)
+                            tc_mma_f8(tmem + h * C::kOReg, vb + ((h * C::kSlice + kt * 32 * C::kRB) >> 4),
+                                      pb + ((kt * 32 * C::kPW) >> 4), idesc,
+                                      kt > 0 ? 1u : (t > 0 ? 1u : 0u));
+                    tc_commit(b_o_done + 8 * (t & 1));
+                    tc_commit(b_v_empty + 8 * s);
+                }
+                __syncwarp();
+                if (++s == vst) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
-        if (!ok) {
+        if (!__all_sync(0xffffffffu, ok)) {
             status_bits |= PA_STATUS_TIMEOUT;
             *abort_flag = 1;
         }
@@ -675,440 +711,339 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         const int row0 = wg * kRW;
         const int tk = threadIdx.x & 127;     // token of the tile, TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        bool ok = true;
-        int g = 0;           // tiles so far, over all stretches
-        Q8Seg sg = first;
-        for (int pos = w; pos < w_end; advance(sg, pos)) {
-            const Range rg = range_of(sg);
-            const int ntiles = rg.ntiles, nblk = rg.nblk, c0 = rg.c0, nrows = rg.nrows;
-            const int32_t *bt = table_of(sg, rg);
-            auto row_of = [&](int r) -> size_t { // row of [S * q_len * H] of local row r
-                const int c = c0 + r;
-                if (p.q_len == 1)
-                    return (size_t)sg.b * p.num_heads + sg.kv * p.group + c;
-                return ((size_t)sg.b * p.q_len + c / p.group) * p.num_heads + sg.kv * p.group +
-                       c % p.group;
-            };
-            if (ntiles == 0) {
-                // No row sees a token of the stretch: an empty partial (m = -inf,
-                // l = 0, o = 0), or a zero output.
-                for (int idx = threadIdx.x; idx < nrows * D; idx += C::kSoft) {
-                    const size_t row = row_of(idx / D);
-                    if (sg.whole) {
-                        static_cast<T *>(p.out)[row * D + idx % D] = E::from_float(0.f);
-                    } else {
-                        const size_t slot = row * p.max_num_partitions + sg.part;
-                        p.tmp_output[slot * D + idx % D] = 0.f;
-                        if (idx % D == 0) {
-                            p.exp_sums[slot] = 0.f;
-                            p.max_logits[slot] = -INFINITY;
-                        }
-                    }
+        // The range's scales (the first S runs meanwhile): the largest V scale of
+        // all, and the first chapter into shared memory.
+        vref = fmaxf(vref, vs_first);
+        for (int j = threadIdx.x + C::kSoft; j < nblk; j += C::kSoft)
+            vref = fmaxf(vref, __ldg(p.v_scales + (size_t)valid_id(__ldg(bt + j)) * p.num_kv_heads + kv));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
+        if (lane == 0)
+            s_vref[warp] = vref;
+        bar_sync(1, C::kSoft);
+#pragma unroll
+        for (int w = 0; w < C::kSoft / 32; ++w)
+            vref = fmaxf(vref, s_vref[w]);
+        const float vref_lg = fast_log2(vref);
+        // Blocks that are not there get ks = 0 and any lv.
+        auto put_scales = [&](int i, float k, float v) {
+            const float lv = fmaxf(fast_log2(v) - vref_lg, kQ8Floor);
+            s_ks[i] = k;
+            s_lv[i] = lv;
+            s_rl[i] = fast_exp2(-lv);
+        };
+        auto load_chapter = [&](int j0, int i0) { // blocks j0 + i, i >= i0
+            for (int i = i0 + threadIdx.x; i < kQ8Chap; i += C::kSoft) {
+                float k = 0.f, v = 0.f;
+                if (j0 + i < nblk) {
+                    const size_t at = (size_t)valid_id(__ldg(bt + j0 + i)) * p.num_kv_heads + kv;
+                    k = __ldg(p.k_scales + at);
+                    v = __ldg(p.v_scales + at);
                 }
-                continue;
+                put_scales(i, k, v);
+                if (j0 + i >= nblk + bpt)
+                    break; // past the last tile
+            }
+        };
+        put_scales(threadIdx.x, ks_first, vs_first);
+        load_chapter(0, C::kSoft);
+        bar_sync(1, C::kSoft);
+        // Rows r >= r_min(token) see the token; a tile that every row sees whole
+        // (and that lies inside the range) skips the test.  Positions from tok0
+        // (a range is less than 2^31 - 128 tokens long: its tiles' ends fit 32 bits).
+        const int rel_a = tokA - tok0, rel_e = tokE - tok0;
+        const int rel_q = L - p.q_len - tok0;
+        const int rel_all = min(rel_e, rel_q + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
+        uint64_t l2[kRW / 2]; // pairs of rows
+#pragma unroll
+        for (int r = 0; r < kRW / 2; ++r)
+            l2[r] = 0;
+        bool ok = true;
+        for (int t = 0; t < ntiles; ++t) {
+            const int j = C::kBuf == 2 ? t & 1 : 0;
+            if (t > 0 && (t * bpt) % kQ8Chap == 0) {
+                // The next chapter of scales (ranges of more than kQ8Chap blocks).
+                bar_sync(1, C::kSoft);
+                load_chapter(t * bpt, 0);
+                bar_sync(1, C::kSoft);
+            }
+            const int at = (t * bpt + (tk >> sh)) & (kQ8Chap - 1); // this token's block
+            const float ks = s_ks[at], lv = s_lv[at], rl = s_rl[at];
+            const int first = t * kQ8Tok; // from tok0
+            const bool full = first >= rel_a && first + kQ8Tok <= rel_all;
+            // First visible row of this thread's token: new token i = (c0 + r) /
+            // group sees it when i >= pos - (L - q_len).
+            int r_min = 0;
+            if (!full) {
+                const int pos = first + tk;
+                const int i0 = pos - rel_q;
+                const long long r0 = i0 > 0 ? (long long)i0 * p.group - c0 : 0;
+                r_min = pos < rel_a || pos >= rel_e || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
             }
 
-            // ---- the stretch's rows and scales.  Q rows -> shared memory in PL parts,
-            // K-major, swizzled (16-byte chunk c of row n at c ^ (n & 7), of 64-byte
-            // rows c ^ (n >> 1 & 3)); a warp per row.  (Every S of the stretch before has
-            // been read, so its MMAs are done with the rows before.)
-            constexpr int kDL = D / 32;                 // consecutive dims of a lane: 2, 4 or 8
-            constexpr int kRows = NR / (C::kSoft / 32); // rows of a warp
-            const int32_t id_first = (int)threadIdx.x < nblk ? __ldg(bt + threadIdx.x) : 0;
-            uint32_t q_raw[kRows][kDL / 2];
+            if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (t & 1),
+                                                             (uint32_t)(t >> 1) & 1u, abort_flag)))
+                ok = false;
+            tc_fence_after();
+            const uint32_t sc = lane_base + C::kSCol + (uint32_t)j * C::kSReg + row0;
+            // Exponents of the stored weights, s + lv + (11 - M); with raw, s + lv.
+            float x[kRW];
+            auto exponents = [&](bool raw) -> float {
+                float top = -INFINITY;
+                uint32_t sr[PL][kRW];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = warp + i * (C::kSoft / 32);
-                const uint32_t *q32 = static_cast<const uint32_t *>(p.query) +
-                                      row_of(r < nrows ? r : 0) * (D / 2) + lane * (kDL / 2);
+                for (int k = 0; k < PL; ++k)
+                    tmem_ld(sc + k * NR, sr[k]);
 #pragma unroll
-                for (int k = 0; k < kDL / 2; ++k)
-                    q_raw[i][k] = r < nrows ? __ldg(q32 + k) : 0u;
-            }
-            float vref = 1.1754943508222875e-38f; // 2^-126, or the stretch's largest V scale
-            float ks_first = 0.f, vs_first = 0.f; // scales of block threadIdx.x
-            if ((int)threadIdx.x < nblk) {
-                const size_t at = (size_t)valid_id(id_first) * p.num_kv_heads + sg.kv;
-                ks_first = __ldg(p.k_scales + at);
-                vs_first = __ldg(p.v_scales + at);
-            }
-            if (pos != w)
-                bar_sync(1, C::kSoft); // the stretch before is stored
+                for (int k = 0; k < PL; ++k)
+                    tmem_wait_ld(sr[k]);
+                const uint64_t ks2 = f2_pack(ks, ks), lv2 = f2_pack(lv, lv);
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = warp + i * (C::kSoft / 32);
-                float x[kDL], m = 0.f;
+                for (int r = 0; r < kRW; r += 4) {
+                    const float4 cf = *reinterpret_cast<const float4 *>(s_cf + row0 + r);
+                    const float4 nm = *reinterpret_cast<const float4 *>(s_nm + row0 + r);
 #pragma unroll
-                for (int k = 0; k < kDL / 2; ++k) {
-                    x[2 * k] = E::lo(q_raw[i][k]);
-                    x[2 * k + 1] = E::hi(q_raw[i][k]);
-                    m = fmaxf(m, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = r + 2 * h;
+                        uint64_t s = f2_pack(__uint_as_float(sr[PL - 1][i]),
+                                             __uint_as_float(sr[PL - 1][i + 1]));
+#pragma unroll
+                        for (int k = PL - 2; k >= 0; --k)
+                            s = f2_fma(s, f2_pack(0.0625f, 0.0625f),
+                                       f2_pack(__uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1])));
+                        const uint64_t add =
+                            raw ? lv2 : f2_add(lv2, h ? f2_pack(nm.z, nm.w) : f2_pack(nm.x, nm.y));
+                        f2_unpack(f2_fma(s, f2_mul(ks2, h ? f2_pack(cf.z, cf.w) : f2_pack(cf.x, cf.y)), add),
+                                  x[i], x[i + 1]);
+                    }
+                }
+                if (!full) {
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r)
+                        x[r] = row0 + r >= r_min ? x[r] : -INFINITY;
                 }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                float f, inv;
-                q_row_scale(m, f, inv);
-                if (lane == 0) {
-                    s_cf[r] = p.scale * inv * kLog2e;
-                    s_nm[r] = -kQ8NoMax;
-                    const size_t row = row_of(r < nrows ? r : 0);
-                    s_row[r] = sg.whole ? row : row * p.max_num_partitions + sg.part;
+                for (int r = 0; r < kRW; r += 2)
+                    top = fmax3(top, x[r], x[r + 1]);
+                return top;
+            };
+            if (t == 0 || bar_any(2 + wg, 128, exponents(false) > kQ8Unit + kQ8Grow)) {
+                // A weight passes 2^4 in some row: M moves to the rows' maxima over
+                // the tile.
+                exponents(true);
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) {
+                    const int m = __reduce_max_sync(0xffffffffu, ordered(x[r]));
+                    if (lane == 0)
+                        s_red[warp][r] = m;
+                }
+                bar_sync(2 + wg, 128);
+                if (tk < kRW) {
+                    int m = s_red[wg * 4][tk];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w)
+                        m = max(m, s_red[wg * 4 + w][tk]);
+                    const float old = s_nm[row0 + tk];
+                    const float now = fminf(old, kQ8Unit - unordered(m));
+                    s_nm[row0 + tk] = now;
+                    s_al[row0 + tk] = fast_exp2(now - old);
+                }
+                bar_sync(2 + wg, 128);
+                if (t > 0) {
+                    // P.V(t - 1) has to land before O is rescaled (tile 0 has no O yet).
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
+                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                        ok = false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 4 * C::kMB; ++k) {
+                        const uint32_t oc = lane_base + (k >> 2) * C::kOReg + (k & 3) * NR + row0;
+#pragma unroll
+                        for (int r8 = 0; r8 < kRW; r8 += 8) {
+                            uint32_t o[8];
+                            tmem_ld(oc + r8, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                o[r] = __float_as_uint(__uint_as_float(o[r]) * s_al[row0 + r8 + r]);
+                            tmem_st(oc + r8, o);
+                        }
+                    }
+                    tmem_st_wait();
                 }
 #pragma unroll
-                for (int k = 0; k < kDL; ++k) // a value that is not finite becomes NaN
-                    x[k] = fabsf(x[k]) <= 3.4028234663852886e38f ? x[k] * f : NAN;
+                for (int r = 0; r < kRW; ++r)
+                    x[r] += s_nm[row0 + r];
 #pragma unroll
-                for (int k = 0; k < PL; ++k) {
-                    const int n = k * NR + r;
-                    const int d = lane * kDL;          // first dim
-                    const int c = (d % C::kRB) >> 4;   // 16-byte chunk
-                    const int sw = C::kRB == 128 ? c ^ (n & 7) : c ^ ((n >> 1) & 3);
-                    const uint32_t dst = q_sm + (d / C::kRB) * (C::kSN * C::kRB) + n * C::kRB +
-                                         (sw << 4) + (d & 15);
+                for (int r = 0; r < kRW; r += 2)
+                    l2[r / 2] = f2_mul(l2[r / 2], f2_pack(s_al[row0 + r], s_al[row0 + r + 1]));
+            }
+
+            // ---- weights, their sums, and their four parts -> this token's row of P,
+            // once P.V(t - kBuf) has read the buffer
+            if (t >= C::kBuf &&
+                !__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((t - C::kBuf) & 1),
+                                                             (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag)))
+                ok = false;
+            const uint32_t prow = p_sm + (uint32_t)j * C::kPBytes + tk * C::kPW;
+            // 16-byte chunk c of the row, as the swizzle places it.
+            auto chunk = [&](int c) -> uint32_t {
+                constexpr int kLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
+                return (uint32_t)(c ^ ((tk >> kLg) & (C::kPW / 16 - 1))) << 4;
+            };
+            uint32_t w[4][kRW / 4]; // part k of rows 4 i .. 4 i + 3
+            const uint64_t rl2 = f2_pack(rl, rl);
 #pragma unroll
-                    for (int h = 0; h < kDL / 2; ++h) {
-                        const uint32_t code = __nv_cvt_float2_to_fp8x2(
-                            make_float2(x[2 * h], x[2 * h + 1]), __NV_SATFINITE, __NV_E4M3);
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 2 * h), "h"((unsigned short)code)
-                                     : "memory");
-                        const uint32_t back = e4m3_to_f16(code);
-                        x[2 * h] = (x[2 * h] - Elem<__half>::lo(back)) * 16.f;
-                        x[2 * h + 1] = (x[2 * h + 1] - Elem<__half>::hi(back)) * 16.f;
+            for (int r = 0; r < kRW; r += 4) {
+                uint32_t h[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float w0 = fast_exp2(x[r + 2 * q]), w1 = fast_exp2(x[r + 2 * q + 1]);
+                    l2[r / 2 + q] = f2_fma(f2_pack(w0, w1), rl2, l2[r / 2 + q]);
+                    h[q] = Elem<__half>::pack(w0, w1);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[k][r / 4] = __byte_perm(h[0], h[1], 0x7531); // upper bytes
+                    if (k < 3) {
+                        h[0] = h2_sub(h[0], h[0] & 0xff00ff00u);
+                        h[1] = h2_sub(h[1], h[1] & 0xff00ff00u);
+                    }
+                }
+            }
+            if constexpr (kRW == 16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int n = k * NR + row0;
+                    const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
+                                 "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
+                                 : "memory");
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(k / 2)),
+                                 "r"(w[k][0]), "r"(w[k][1]), "r"(w[k + 1][0]), "r"(w[k + 1][1])
+                                 : "memory");
+            }
+            if (t == ntiles - 1) {
+                // Tile rows past the range (unloaded blocks, slots past the sequence
+                // end) may hold anything: zero them in V so that 0 * NaN cannot reach O.
+                const int vt = tokE - (tok0 + t * kQ8Tok);
+                if (vt < kQ8Tok) {
+                    const int s = t % vst;
+                    // The parity wait is unambiguous once the stage's previous fill has
+                    // landed, which P.V(t - kBuf), done by now, says for a ring of kBuf
+                    // stages or more; a shorter one waits for P.V(t - 1) first.
+                    if (vst < C::kBuf && t > 0 &&
+                        !__all_sync(0xffffffffu,
+                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
+                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                        ok = false;
+                    if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_v_full + 8 * s,
+                                                                     (uint32_t)(t / vst) & 1u, abort_flag)))
+                        ok = false;
+                    const uint32_t vb = v_sm + (uint32_t)s * C::kTile;
+                    constexpr int kChunks = C::kRB / 16;
+                    const int n = (kQ8Tok - vt) * kChunks * C::kSlices;
+                    for (int idx = threadIdx.x; idx < n; idx += C::kSoft) {
+                        const int rest = idx / C::kSlices;
+                        st_shared_zero16(vb + (idx % C::kSlices) * C::kSlice +
+                                         (vt + rest / kChunks) * C::kRB + (rest % kChunks) * 16);
                     }
                 }
             }
             fence_proxy_async();
-            mbar_arrive(b_q_full);
-            // The largest V scale of all, and the first chapter into shared memory (the
-            // first S runs meanwhile).
-            vref = fmaxf(vref, vs_first);
-            for (int j = threadIdx.x + C::kSoft; j < nblk; j += C::kSoft)
-                vref = fmaxf(vref, __ldg(p.v_scales + (size_t)valid_id(__ldg(bt + j)) * p.num_kv_heads +
-                                         sg.kv));
+            tc_fence_before();
+            mbar_arrive(b_p_full + 8 * (t & 1));
+        }
+        // ---- l over the tokens while the last P.V runs.  In a warp: lanes trade
+        // halves of their rows until each holds one row's sum over a group of
+        // lanes, then those groups meet; warps meet in shared memory.
+        constexpr int kLg = kRW == 16 ? 4 : 3;
+        float l_run[kRW];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
-            if (lane == 0)
-                s_vref[warp] = vref;
-            bar_sync(1, C::kSoft);
+        for (int r = 0; r < kRW; r += 2)
+            f2_unpack(l2[r / 2], l_run[r], l_run[r + 1]);
 #pragma unroll
-            for (int w8 = 0; w8 < C::kSoft / 32; ++w8)
-                vref = fmaxf(vref, s_vref[w8]);
-            const float vref_lg = fast_log2(vref);
-            // Blocks that are not there get ks = 0 and any lv.
-            auto put_scales = [&](int i, float k, float v) {
-                const float lv = fmaxf(fast_log2(v) - vref_lg, kQ8Floor);
-                s_ks[i] = k;
-                s_lv[i] = lv;
-                s_rl[i] = fast_exp2(-lv);
-            };
-            auto load_chapter = [&](int j0, int i0) { // blocks j0 + i, i >= i0, up to the last tile's end
-                for (int i = i0 + threadIdx.x; i < kQ8Chap && j0 + i < nblk + bpt; i += C::kSoft) {
-                    float k = 0.f, v = 0.f;
-                    if (j0 + i < nblk) {
-                        const size_t at =
-                            (size_t)valid_id(__ldg(bt + j0 + i)) * p.num_kv_heads + sg.kv;
-                        k = __ldg(p.k_scales + at);
-                        v = __ldg(p.v_scales + at);
-                    }
-                    put_scales(i, k, v);
-                }
-            };
-            put_scales(threadIdx.x, ks_first, vs_first);
-            load_chapter(0, C::kSoft);
-            bar_sync(1, C::kSoft);
-            // Rows r >= r_min(token) see the token; a tile that every row sees whole
-            // skips the test.  Positions from tok0.
-            const int rel_e = rg.tok_e - rg.tok0;
-            const int rel_q = sg.len - p.q_len - rg.tok0;
-            const int rel_all = min(rel_e, rel_q + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
-            uint64_t l2[kRW / 2]; // pairs of rows
+        for (int i = 0; i < kLg; ++i) {
+            const int half = kRW >> (i + 1), off = 16 >> i;
+            const bool up = (lane & off) != 0;
 #pragma unroll
-            for (int r = 0; r < kRW / 2; ++r)
-                l2[r] = 0;
-            for (int t = 0; t < ntiles; ++t, ++g) {
-                const int j = C::kBuf == 2 ? g & 1 : 0;
-                if (t > 0 && (t * bpt) % kQ8Chap == 0) {
-                    // The next chapter of scales (stretches of more than kQ8Chap blocks).
-                    bar_sync(1, C::kSoft);
-                    load_chapter(t * bpt, 0);
-                    bar_sync(1, C::kSoft);
-                }
-                const int at = (t * bpt + (tk >> sh)) & (kQ8Chap - 1); // this token's block
-                const float ks = s_ks[at], lv = s_lv[at], rl = s_rl[at];
-                const int from = t * kQ8Tok; // from tok0
-                const bool full = from + kQ8Tok <= rel_all;
-                // First visible row of this thread's token: new token i = (c0 + r) /
-                // group sees it when i >= pos - (L - q_len).
-                int r_min = 0;
-                if (!full) {
-                    const int at_tok = from + tk;
-                    const int i0 = at_tok - rel_q;
-                    const long long r0 = i0 > 0 ? (long long)i0 * p.group - c0 : 0;
-                    r_min = at_tok >= rel_e || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
-                }
-
-                if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (g & 1),
-                                                                 (uint32_t)(g >> 1) & 1u, abort_flag)))
-                    ok = false;
-                tc_fence_after();
-                const uint32_t sc = lane_base + C::kSCol + (uint32_t)j * C::kSReg + row0;
-                // Exponents of the stored weights, s + lv + (11 - M); with raw, s + lv.
-                float x[kRW];
-                auto exponents = [&](bool raw) -> float {
-                    float top = -INFINITY;
-                    uint32_t sr[PL][kRW];
-#pragma unroll
-                    for (int k = 0; k < PL; ++k)
-                        tmem_ld(sc + k * NR, sr[k]);
-#pragma unroll
-                    for (int k = 0; k < PL; ++k)
-                        tmem_wait_ld(sr[k]);
-                    const uint64_t ks2 = f2_pack(ks, ks), lv2 = f2_pack(lv, lv);
-#pragma unroll
-                    for (int r = 0; r < kRW; r += 4) {
-                        const float4 cf = *reinterpret_cast<const float4 *>(s_cf + row0 + r);
-                        const float4 nm = *reinterpret_cast<const float4 *>(s_nm + row0 + r);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int i = r + 2 * h;
-                            uint64_t s = f2_pack(__uint_as_float(sr[PL - 1][i]),
-                                                 __uint_as_float(sr[PL - 1][i + 1]));
-#pragma unroll
-                            for (int k = PL - 2; k >= 0; --k)
-                                s = f2_fma(s, f2_pack(0.0625f, 0.0625f),
-                                           f2_pack(__uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1])));
-                            const uint64_t add =
-                                raw ? lv2 : f2_add(lv2, h ? f2_pack(nm.z, nm.w) : f2_pack(nm.x, nm.y));
-                            f2_unpack(f2_fma(s, f2_mul(ks2, h ? f2_pack(cf.z, cf.w) : f2_pack(cf.x, cf.y)), add),
-                                      x[i], x[i + 1]);
-                        }
-                    }
-                    if (!full) {
-#pragma unroll
-                        for (int r = 0; r < kRW; ++r)
-                            x[r] = row0 + r >= r_min ? x[r] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int r = 0; r < kRW; r += 2)
-                        top = fmax3(top, x[r], x[r + 1]);
-                    return top;
-                };
-                if (t == 0 || bar_any(2 + wg, 128, exponents(false) > kQ8Unit + kQ8Grow)) {
-                    // A weight passes 2^4 in some row: M moves to the rows' maxima over
-                    // the tile.
-                    exponents(true);
-#pragma unroll
-                    for (int r = 0; r < kRW; ++r) {
-                        const int m = __reduce_max_sync(0xffffffffu, ordered(x[r]));
-                        if (lane == 0)
-                            s_red[warp][r] = m;
-                    }
-                    bar_sync(2 + wg, 128);
-                    if (tk < kRW) {
-                        int m = s_red[wg * 4][tk];
-#pragma unroll
-                        for (int w = 1; w < 4; ++w)
-                            m = max(m, s_red[wg * 4 + w][tk]);
-                        const float old = s_nm[row0 + tk];
-                        const float now = fminf(old, kQ8Unit - unordered(m));
-                        s_nm[row0 + tk] = now;
-                        s_al[row0 + tk] = fast_exp2(now - old);
-                    }
-                    bar_sync(2 + wg, 128);
-                    if (t > 0) {
-                        // P.V(t - 1) has to land before O is rescaled (tile 0 has no O yet).
-                        if (!__all_sync(0xffffffffu,
-                                        mbar_wait_abortable(b_o_done + 8 * ((g - 1) & 1),
-                                                            (uint32_t)((g - 1) >> 1) & 1u, abort_flag)))
-                            ok = false;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < 4 * C::kMB; ++k) {
-                            const uint32_t oc = lane_base + (k >> 2) * C::kOReg + (k & 3) * NR + row0;
-#pragma unroll
-                            for (int r8 = 0; r8 < kRW; r8 += 8) {
-                                uint32_t o[8];
-                                tmem_ld(oc + r8, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int r = 0; r < 8; ++r)
-                                    o[r] = __float_as_uint(__uint_as_float(o[r]) * s_al[row0 + r8 + r]);
-                                tmem_st(oc + r8, o);
-                            }
-                        }
-                        tmem_st_wait();
-                    }
-#pragma unroll
-                    for (int r = 0; r < kRW; ++r)
-                        x[r] += s_nm[row0 + r];
-#pragma unroll
-                    for (int r = 0; r < kRW; r += 2)
-                        l2[r / 2] = f2_mul(l2[r / 2], f2_pack(s_al[row0 + r], s_al[row0 + r + 1]));
-                }
-
-                // ---- weights, their sums, and their four parts -> this token's row of P,
-                // once P.V(g - kBuf) has read the buffer (the stretches before are done)
-                if (t >= C::kBuf &&
-                    !__all_sync(0xffffffffu,
-                                mbar_wait_abortable(b_o_done + 8 * ((g - C::kBuf) & 1),
-                                                    (uint32_t)((g - C::kBuf) >> 1) & 1u, abort_flag)))
-                    ok = false;
-                const uint32_t prow = p_sm + (uint32_t)j * C::kPBytes + tk * C::kPW;
-                // 16-byte chunk c of the row, as the swizzle places it.
-                auto chunk = [&](int c) -> uint32_t {
-                    constexpr int kLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
-                    return (uint32_t)(c ^ ((tk >> kLg) & (C::kPW / 16 - 1))) << 4;
-                };
-                uint32_t w[4][kRW / 4]; // part k of rows 4 i .. 4 i + 3
-                const uint64_t rl2 = f2_pack(rl, rl);
-#pragma unroll
-                for (int r = 0; r < kRW; r += 4) {
-                    uint32_t h[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float w0 = fast_exp2(x[r + 2 * q]), w1 = fast_exp2(x[r + 2 * q + 1]);
-                        l2[r / 2 + q] = f2_fma(f2_pack(w0, w1), rl2, l2[r / 2 + q]);
-                        h[q] = Elem<__half>::pack(w0, w1);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        w[k][r / 4] = __byte_perm(h[0], h[1], 0x7531); // upper bytes
-                        if (k < 3) {
-                            h[0] = h2_sub(h[0], h[0] & 0xff00ff00u);
-                            h[1] = h2_sub(h[1], h[1] & 0xff00ff00u);
-                        }
-                    }
-                }
-                if constexpr (kRW == 16) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int n = k * NR + row0;
-                        const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
-                                     "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
-                                     : "memory");
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; k += 2)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(k / 2)),
-                                     "r"(w[k][0]), "r"(w[k][1]), "r"(w[k + 1][0]), "r"(w[k + 1][1])
-                                     : "memory");
-                }
-                if (t == ntiles - 1) {
-                    // Tile rows past the range (unloaded blocks, slots past the sequence
-                    // end) may hold anything: zero them in V so that 0 * NaN cannot reach O.
-                    const int vt = rel_e - from;
-                    if (vt < kQ8Tok) {
-                        const int s = g % vst;
-                        // The parity wait is unambiguous once the stage's previous fill has
-                        // landed, which P.V(g - kBuf), done by now, says for a ring of kBuf
-                        // stages or more; a shorter one waits for P.V(g - 1) first.
-                        if (vst < C::kBuf && t > 0 &&
-                            !__all_sync(0xffffffffu,
-                                        mbar_wait_abortable(b_o_done + 8 * ((g - 1) & 1),
-                                                            (uint32_t)((g - 1) >> 1) & 1u, abort_flag)))
-                            ok = false;
-                        if (!__all_sync(0xffffffffu,
-                                        mbar_wait_abortable(b_v_full + 8 * s, (uint32_t)(g / vst) & 1u,
-                                                            abort_flag)))
-                            ok = false;
-                        const uint32_t vb = v_sm + (uint32_t)s * C::kTile;
-                        constexpr int kChunks = C::kRB / 16;
-                        const int n = (kQ8Tok - vt) * kChunks * C::kSlices;
-                        for (int idx = threadIdx.x; idx < n; idx += C::kSoft) {
-                            const int rest = idx / C::kSlices;
-                            st_shared_zero16(vb + (idx % C::kSlices) * C::kSlice +
-                                             (vt + rest / kChunks) * C::kRB + (rest % kChunks) * 16);
-                        }
-                    }
-                }
-                fence_proxy_async();
-                tc_fence_before();
-                mbar_arrive(b_p_full + 8 * (g & 1));
-            }
-
-            // ---- l over the tokens while the last P.V runs.  In a warp: lanes trade
-            // halves of their rows until each holds one row's sum over a group of
-            // lanes, then those groups meet; warps meet in shared memory.
-            constexpr int kLg = kRW == 16 ? 4 : 3;
-            float l_run[kRW];
-#pragma unroll
-            for (int r = 0; r < kRW; r += 2)
-                f2_unpack(l2[r / 2], l_run[r], l_run[r + 1]);
-#pragma unroll
-            for (int i = 0; i < kLg; ++i) {
-                const int half = kRW >> (i + 1), off = 16 >> i;
-                const bool up = (lane & off) != 0;
-#pragma unroll
-                for (int r = 0; r < half; ++r) {
-                    const float give = up ? l_run[r] : l_run[r + half];
-                    const float keep = up ? l_run[r + half] : l_run[r];
-                    l_run[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                }
-            }
-#pragma unroll
-            for (int off = 16 >> kLg; off > 0; off >>= 1)
-                l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
-            // Lane bits 4, 3, .. chose the halves: its row is lane >> (5 - kLg).
-            if ((lane & ((32 >> kLg) - 1)) == 0)
-                s_part[warp][lane >> (5 - kLg)] = l_run[0];
-            bar_sync(2 + wg, 128);
-            if (tk < kRW) {
-                float sum = s_part[wg * 4][tk];
-#pragma unroll
-                for (int w4 = 1; w4 < 4; ++w4)
-                    sum += s_part[wg * 4 + w4][tk];
-                const int r = row0 + tk;
-                s_inv[r] = sum > 0.f ? vref / sum : 0.f; // O and l hold weights in the same unit
-                if (!sg.whole && r < nrows) {
-                    p.exp_sums[s_row[r]] = sum * 4.8828125e-4f; // 2^-11
-                    p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Unit - s_nm[r]) * kQ8Ln2 : -INFINITY;
-                }
-            }
-            bar_sync(2 + wg, 128);
-            // The stretch's last P.V.
-            if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((g - 1) & 1),
-                                                             (uint32_t)((g - 1) >> 1) & 1u, abort_flag)))
-                ok = false;
-            tc_fence_after();
-
-            // ---- epilogue: thread = dim, O of its rows from the four parts
-            if (ok && tk < D) {
-#pragma unroll 1
-                for (int h = 0; h < C::kMB; ++h) {
-                    const int d = h * 128 + tk;
-#pragma unroll 1
-                    for (int r8 = 0; r8 < kRW; r8 += 8) {
-                        uint32_t o[4][8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tmem_ld(lane_base + h * C::kOReg + k * NR + row0 + r8, o[k]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tmem_wait_ld(o[k]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = row0 + r8 + i;
-                            if (r < nrows) {
-                                const float v = ((__uint_as_float(o[3][i]) + __uint_as_float(o[2][i])) +
-                                                 (__uint_as_float(o[1][i]) + __uint_as_float(o[0][i]))) *
-                                                s_inv[r];
-                                if (sg.whole)
-                                    static_cast<T *>(p.out)[s_row[r] * D + d] = E::from_float(v);
-                                else
-                                    p.tmp_output[s_row[r] * D + d] = v;
-                            }
-                        }
-                    }
-                }
+            for (int r = 0; r < half; ++r) {
+                const float give = up ? l_run[r] : l_run[r + half];
+                const float keep = up ? l_run[r + half] : l_run[r];
+                l_run[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
             }
         }
+#pragma unroll
+        for (int off = 16 >> kLg; off > 0; off >>= 1)
+            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
+        // Lane bits 4, 3, .. chose the halves: its row is lane >> (5 - kLg).
+        if ((lane & ((32 >> kLg) - 1)) == 0)
+            s_part[warp][lane >> (5 - kLg)] = l_run[0];
+        bar_sync(2 + wg, 128);
+        if (tk < kRW) {
+            float sum = s_part[wg * 4][tk];
+#pragma unroll
+            for (int w = 1; w < 4; ++w)
+                sum += s_part[wg * 4 + w][tk];
+            const int r = row0 + tk;
+            s_inv[r] = sum > 0.f ? vref / sum : 0.f; // O and l hold weights in the same unit
+            if (V1) {
+                s_ml[r] = sum > 0.f ? kQ8Unit - s_nm[r] : -INFINITY;
+                s_ml[NR + r] = sum;
+            } else if (r < nrows) {
+                p.exp_sums[s_row[r]] = sum * 4.8828125e-4f; // 2^-11
+                p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Unit - s_nm[r]) * kQ8Ln2 : -INFINITY;
+            }
+        }
+        bar_sync(2 + wg, 128);
+        // P.V(ntiles - 1), the last MMA.
+        if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((ntiles - 1) & 1),
+                                                    (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag)))
+            ok = false;
+        tc_fence_after();
         if (!ok) {
             status_bits |= PA_STATUS_TIMEOUT;
             *abort_flag = 1;
+        }
+
+        // ---- epilogue: thread = dim, O of its rows from the three parts
+        if (ok && tk < D) {
+#pragma unroll 1
+            for (int h = 0; h < C::kMB; ++h) {
+                const int d = h * 128 + tk;
+#pragma unroll 1
+                for (int r8 = 0; r8 < kRW; r8 += 8) {
+                    uint32_t o[4][8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tmem_ld(lane_base + h * C::kOReg + k * NR + row0 + r8, o[k]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tmem_wait_ld(o[k]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = row0 + r8 + i;
+                        if (r < nrows) {
+                            const float v = ((__uint_as_float(o[3][i]) + __uint_as_float(o[2][i])) +
+                                             (__uint_as_float(o[1][i]) + __uint_as_float(o[0][i]))) *
+                                            s_inv[r];
+                            if (V1 && ways > 1) // every tile of the rings is read by now
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem0 + (r * D + d) * 4), "f"(v)
+                                             : "memory");
+                            else if (V1)
+                                static_cast<T *>(p.out)[s_row[r] * D + d] = E::from_float(v);
+                            else
+                                p.tmp_output[s_row[r] * D + d] = v;
+                        }
+                    }
+                }
+            }
         }
     }
 
@@ -1120,19 +1055,25 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
     }
+    if (V1 && ways > 1)
+        join_cluster<D, NR>(smem0, smem_addr(s_ml), part, ways, nrows, static_cast<T *>(p.out), row_of);
 }
 
 // Kernel and shared memory of one head_dim for NR = 8, 16, 32 or 64 rows (64
 // up to head_dim 128).
 template <int D, int NR>
-static Q8TcKernel q8_tc_pick(int dtype)
+static Q8TcKernel q8_tc_pick(int dtype, bool v1)
 {
     if (dtype == PA_BF16) {
         using C = Q8Cfg<D, NR, 2>;
-        return {reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2>), C::kThreads, C::kCtas, C::kFixed};
+        return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, true>)
+                   : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, false>),
+                C::kThreads, C::kCtas, C::kFixed};
     }
     using C = Q8Cfg<D, NR, 3>;
-    return {reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3>), C::kThreads, C::kCtas, C::kFixed};
+    return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, true>)
+               : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, false>),
+            C::kThreads, C::kCtas, C::kFixed};
 }
 
 } // namespace pa

@@ -3,12 +3,12 @@
 
 namespace pa {
 
-Q8TcKernel q8_tc_d256(int rows, int dtype)
+Q8TcKernel q8_tc_d256(int rows, int dtype, bool v1)
 {
     switch (rows) {
-    case 8: return q8_tc_pick<256, 8>(dtype);
-    case 16: return q8_tc_pick<256, 16>(dtype);
-    case 32: return q8_tc_pick<256, 32>(dtype);
+    case 8: return q8_tc_pick<256, 8>(dtype, v1);
+    case 16: return q8_tc_pick<256, 16>(dtype, v1);
+    case 32: return q8_tc_pick<256, 32>(dtype, v1);
     default: return {nullptr, 0, 0, 0};
     }
 }

@@ -3,13 +3,13 @@
 
 namespace pa {
 
-Q8TcKernel q8_tc_d64(int rows, int dtype)
+Q8TcKernel q8_tc_d64(int rows, int dtype, bool v1)
 {
     switch (rows) {
-    case 8: return q8_tc_pick<64, 8>(dtype);
-    case 16: return q8_tc_pick<64, 16>(dtype);
-    case 32: return q8_tc_pick<64, 32>(dtype);
-    case 64: return q8_tc_pick<64, 64>(dtype);
+    case 8: return q8_tc_pick<64, 8>(dtype, v1);
+    case 16: return q8_tc_pick<64, 16>(dtype, v1);
+    case 32: return q8_tc_pick<64, 32>(dtype, v1);
+    case 64: return q8_tc_pick<64, 64>(dtype, v1);
     default: return {nullptr, 0, 0, 0};
     }
 }

@@ -36,6 +36,12 @@ def test_refused_before_launch(cuda_lib, kw, code):
     assert _call(cuda_lib.load(), **kw) == code
 
 
+def test_partition_arguments(cuda_lib):
+    for bad in ((0, 1, 8, 2, 128, 1000, 512), (1, 0, 8, 2, 128, 1000, 512), (1, 1, 7, 2, 128, 1000, 512),
+                (1, 1, 8, 2, 0, 1000, 512), (1, 1, 8, 2, 128, -1, 512), (1, 1, 8, 2, 128, 1000, 0)):
+        assert cuda_lib.load().pa_decode_q8_partition(*bad) == -1
+
+
 def test_binding_refuses(cuda_lib):
     kc, vc, ks, vs, tables, lens = cu.cache8([40, 3])
     q = torch.zeros((2, 4, 64), dtype=F16)
@@ -101,6 +107,26 @@ def test_shapes(pa, D, bs, dtype):
     check(pa, LENS, D=D, bs=bs, dtype=dtype)                        # several partitions, tails inside blocks
     check(pa, LENS, D=D, bs=bs, dtype=dtype, P=100, G=12, KV=1)     # two n-tiles, partitions across blocks
     check(pa, [40, 0, 33], D=D, bs=bs, dtype=dtype, P=512, G=1)     # one partition
+
+
+@gpu
+@pytest.mark.parametrize("G,Q,D,bs,dtype", [(4, 1, 128, 16, BF16), (16, 1, 64, 8, F16), (1, 6, 256, 64, BF16),
+                                            (8, 12, 128, 32, F16), (64, 1, 128, 16, BF16)])
+@pytest.mark.parametrize("P", [64, 200, 333])
+def test_long_sequences_in_partitions(pa, G, Q, D, bs, dtype, P):
+    """V2: partitions of one tile, ends inside blocks and inside tiles, partitions that hold nothing."""
+    lens = [6000, 0, 3, 2500]
+    assert pa.pa_decode_q8_partition(4, Q, G, 1, D, 6000 // bs * bs, P) > 0
+    check(pa, lens, Q=Q, G=G, KV=1, D=D, bs=bs, dtype=dtype, P=P, scales="any")
+
+
+@gpu
+@pytest.mark.parametrize("G,Q,D,bs", [(4, 1, 64, 64), (5, 3, 128, 8), (2, 16, 256, 16), (32, 2, 128, 32)])
+@pytest.mark.parametrize("longest", [128, 129, 400, 1000, 1300])
+def test_sequences_shared_by_a_cluster(pa, G, Q, D, bs, longest):
+    """V1 with 1 to 8 CTAs per sequence and KV head, some without a token."""
+    check(pa, [longest, 130, 0, 1], Q=Q, G=G, KV=1, D=D, bs=bs, P=2048, scales="any")
+    check(pa, [longest], Q=Q, G=G, KV=2, D=D, bs=bs, P=2048, dtype=F16)
 
 
 @gpu
@@ -204,6 +230,14 @@ def test_same_bits_every_time_and_under_a_graph(pa, Q, G):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@gpu
+def test_partitions_never_finer(pa):
+    for S, Q, H, KV, L, P in ((1, 1, 32, 4, 100000, 512), (32, 1, 32, 8, 8192, 512), (32, 16, 32, 8, 8192, 512),
+                              (2, 2048, 32, 8, 32768, 512), (1, 1, 8, 2, 1000, 512), (64, 1, 64, 8, 32768, 1000)):
+        p = pa.pa_decode_q8_partition(S, Q, H, KV, 128, L, P)
+        assert p == 0 or p >= P
 
 
 @gpu

@@ -1,4 +1,5 @@
-"""ctypes binding of libpa_decode.so (the C ABI in include/pa_decode.h).
+"""Binding of libpa_decode.so (the C ABI in include/pa_decode.h): ctypes, and for the
+operators over caches that a serving loop calls per token a compiled one (csrc/pa_bind.cpp).
 
 Argument marshalling only: every step of the decode runs in the library's
 CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory
@@ -356,129 +357,19 @@ def pa_decode_v2_static(query, key_cache, value_cache, block_tables, seq_lens, s
 
 # ---------------------------------------------------------------- filling a cache; 8-bit caches
 
-_E4M3 = torch.float8_e4m3fn
+_bind = None
 
 
-def _same_device(tensors):
-    """The device index all of ``tensors`` (None entries aside) are on."""
-    index = -1
-    for t in tensors:
-        if t is None:
-            continue
-        i = t.get_device()
-        if i < 0:
-            raise ValueError("all tensors must be CUDA tensors")
-        if i != index:
-            if index >= 0:
-                raise ValueError("all tensors must be on one device")
-            index = i
-    return index
-
-
-def _call(name, index, stream, args):
-    """Calls entry point ``name`` with the tensors' device current, on ``stream`` (default: that
-    device's current stream)."""
-    fn = getattr(_lib or load(), name)
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _call(name, index, stream, args)
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    rc = fn(*args, handle)
-    if rc != PA_OK:
-        raise PagedAttentionError(name, rc)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _cache_args(key_cache, value_cache, block_tables, seq_lens, dtype, k_scales=None,
-                v_scales=None):
-    """(num_seqs, num_kv_heads, head_dim, num_blocks, block_size, max_blocks) after the checks."""
-    nb, KV, bs, D = key_cache.shape
-    if key_cache.dtype != dtype or value_cache.dtype != dtype:
-        raise TypeError(f"key_cache and value_cache must be {dtype}")
-    if value_cache.shape != key_cache.shape:
-        raise ValueError("cache shapes must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    if block_tables.dim() != 2 or seq_lens.dim() != 1 or block_tables.shape[0] != seq_lens.shape[0]:
-        raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
-    if seq_lens.shape[0] == 0:
-        raise ValueError("there must be at least one sequence")
-    if not (key_cache.is_contiguous() and value_cache.is_contiguous()
-            and block_tables.is_contiguous() and seq_lens.is_contiguous()):
-        raise ValueError("caches, block_tables and seq_lens must be contiguous")
-    if k_scales is not None:
-        if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32:
-            raise TypeError("k_scales and v_scales must be float32")
-        if k_scales.shape != (nb, KV) or v_scales.shape != (nb, KV) or \
-                not k_scales.is_contiguous() or not v_scales.is_contiguous():
-            raise ValueError("k_scales and v_scales must be contiguous [num_blocks, num_kv_heads]")
-    return seq_lens.shape[0], KV, D, nb, bs, block_tables.shape[1]
-
-
-def _token_rows(t, what, heads, head_dim, dtype):
-    """(token rows, elements between them) of ``t``, [tokens, heads, head_dim] or
-    [num_seqs, q_len, heads, head_dim]."""
-    if t.dtype != dtype:
-        raise TypeError("key, value, query and query_out must share one dtype: float16 or bfloat16")
-    shape, stride = t.shape, t.stride()
-    if len(shape) not in (3, 4) or shape[-1] != head_dim or (heads and shape[-2] != heads):
-        raise ValueError(f"{what} must be [tokens, heads, head_dim] or [num_seqs, q_len, heads, head_dim]")
-    if stride[-1] != 1 or (shape[-2] > 1 and stride[-2] != head_dim):
-        raise ValueError(f"{what}: a token's heads and dims must be contiguous")
-    n, step = shape[0], stride[0]
-    if len(shape) == 4:
-        if shape[1] > 1:
-            if shape[0] > 1 and step != shape[1] * stride[1]:
-                raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
-            step = stride[1]
-        n *= shape[1]
-    return n, step if n > 1 else shape[-2] * head_dim
-
-
-def _append(name, key, value, block_tables, seq_lens, key_cache, value_cache, k_scales, v_scales,
-            cos_sin, interleaved, query, query_out, token_starts, status, stream):
-    dtype = key.dtype
-    if dtype not in _DTYPE:
-        raise TypeError("key must be float16 or bfloat16")
-    index = _same_device((key, value, block_tables, seq_lens, key_cache, value_cache, k_scales,
-                          v_scales, cos_sin, query, query_out, token_starts, status))
-    S, KV, D, nb, bs, mb = _cache_args(key_cache, value_cache, block_tables, seq_lens,
-                                       dtype if k_scales is None else _E4M3, k_scales, v_scales)
-    n, k_step = _token_rows(key, "key", KV, D, dtype)
-    nv, v_step = _token_rows(value, "value", KV, D, dtype)
-    if nv != n:
-        raise ValueError("key and value must have the same tokens")
-    H = q_step = o_step = 0
-    if query is not None or query_out is not None:
-        if query is None or query_out is None:
-            raise ValueError("query and query_out go together")
-        H = query.shape[-2]
-        nq, q_step = _token_rows(query, "query", H, D, dtype)
-        no, o_step = _token_rows(query_out, "query_out", H, D, dtype)
-        if nq != n or no != n:
-            raise ValueError("key, query and query_out must have the same tokens")
-    if token_starts is not None:
-        if token_starts.dtype != torch.int32 or token_starts.shape != (S + 1,) or \
-                not token_starts.is_contiguous():
-            raise ValueError("token_starts must be a contiguous int32 [num_seqs + 1]")
-    elif (n != S * key.shape[1] or key.shape[0] != S) if key.dim() == 4 else n % S:
-        raise ValueError("without token_starts every sequence has the same number of tokens")
-    rotary = positions = 0
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 [max_positions, rotary_dim]")
-        positions, rotary = cos_sin.shape
-    args = [key.data_ptr(), value.data_ptr(), k_step, v_step, _addr(query), _addr(query_out),
-            q_step, o_step, _addr(cos_sin), rotary, positions, 1 if interleaved else 0,
-            block_tables.data_ptr(), seq_lens.data_ptr(), _addr(token_starts), n, S, H, KV, D, nb,
-            bs, mb, _DTYPE[dtype], key_cache.data_ptr(), value_cache.data_ptr()]
-    if k_scales is not None:
-        args += [k_scales.data_ptr(), v_scales.data_ptr()]
-    args.append(_addr(status))
-    _call(name, index, stream, args)
+def _load_bind():
+    """The compiled side of these three (csrc/pa_bind.cpp): checks and marshals the tensors."""
+    global _bind
+    load()
+    try:
+        from . import _bind as module
+    except ImportError as e:
+        raise ImportError(f"{_PKG}/_bind.so cannot be loaded: run paged_kv_decode_v2_gb300.build.build()") from e
+    _bind = module
+    return module
 
 
 def pa_kv_append(key, value, block_tables, seq_lens, key_cache, value_cache, cos_sin=None,
@@ -491,8 +382,10 @@ def pa_kv_append(key, value, block_tables, seq_lens, key_cache, value_cache, cos
     same number of tokens for every sequence), or [S, q_len, ..., D]; tokens may be strided.
     ``seq_lens`` already counts the new tokens.
     """
-    _append("pa_kv_append", key, value, block_tables, seq_lens, key_cache, value_cache, None, None,
-            cos_sin, interleaved, query, query_out, token_starts, status, stream)
+    rc = (_bind or _load_bind()).append(key, value, block_tables, seq_lens, key_cache, value_cache, None, None,
+                                        cos_sin, interleaved, query, query_out, token_starts, status, stream)
+    if rc:
+        raise PagedAttentionError("pa_kv_append", rc)
 
 
 def pa_kv_append_q8(key, value, block_tables, seq_lens, key_cache, value_cache, k_scales, v_scales,
@@ -500,10 +393,11 @@ def pa_kv_append_q8(key, value, block_tables, seq_lens, key_cache, value_cache, 
                     status=None, stream=None):
     """pa_kv_append into an 8-bit cache: float8_e4m3fn caches and float32 scales
     [num_blocks, KV], powers of two that this call sets or raises."""
-    if k_scales is None or v_scales is None:
-        raise ValueError("k_scales and v_scales are needed")
-    _append("pa_kv_append_q8", key, value, block_tables, seq_lens, key_cache, value_cache, k_scales,
-            v_scales, cos_sin, interleaved, query, query_out, token_starts, status, stream)
+    rc = (_bind or _load_bind()).append_q8(key, value, block_tables, seq_lens, key_cache, value_cache, k_scales,
+                                           v_scales, cos_sin, interleaved, query, query_out, token_starts, status,
+                                           stream)
+    if rc:
+        raise PagedAttentionError("pa_kv_append_q8", rc)
 
 
 def pa_decode_q8(query, key_cache, value_cache, k_scales, v_scales, block_tables, seq_lens, scale,
@@ -511,34 +405,11 @@ def pa_decode_q8(query, key_cache, value_cache, k_scales, v_scales, block_tables
                  status=None, stream=None):
     """pa_decode (query [S, H, D]) or pa_decode_mq (query [S, Q, H, D]) over an 8-bit cache:
     float8_e4m3fn caches and float32 scales [num_blocks, KV]."""
-    dtype = query.dtype
-    if dtype not in _DTYPE or out.dtype != dtype:
-        raise TypeError("query and out must share one dtype: float16 or bfloat16")
-    index = _same_device((query, key_cache, value_cache, k_scales, v_scales, block_tables, seq_lens,
-                          out, tmp_output, exp_sums, max_logits, status))
-    S, KV, D, nb, bs, mb = _cache_args(key_cache, value_cache, block_tables, seq_lens, _E4M3,
-                                       k_scales, v_scales)
-    shape = query.shape
-    if len(shape) not in (3, 4) or shape[0] != S or shape[-1] != D:
-        raise ValueError("query must be [num_seqs, num_heads, head_dim] or "
-                         "[num_seqs, q_len, num_heads, head_dim]")
-    q_len, H = (1, shape[1]) if len(shape) == 3 else (shape[1], shape[2])
-    if out.shape != shape or not query.is_contiguous() or not out.is_contiguous():
-        raise ValueError("query and out must be contiguous and of one shape")
-    parts = 0
-    if tmp_output is not None:
-        parts = tmp_output.shape[-2]
-        rows = S * q_len * H
-        for t, n in ((tmp_output, rows * parts * D), (exp_sums, rows * parts),
-                     (max_logits, rows * parts)):
-            if t is None or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < n:
-                raise ValueError("tmp_output, exp_sums and max_logits must be what alloc_workspace "
-                                 "returns for these sizes")
-    _call("pa_decode_q8", index, stream,
-          [query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
-           v_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), S, q_len, H, KV, D,
-           nb, bs, mb, max_seq_len_hint, scale, partition_size, _DTYPE[dtype], out.data_ptr(),
-           _addr(tmp_output), _addr(exp_sums), _addr(max_logits), parts, _addr(status)])
+    rc = (_bind or _load_bind()).decode_q8(query, key_cache, value_cache, k_scales, v_scales, block_tables, seq_lens,
+                                           scale, partition_size, out, tmp_output, exp_sums, max_logits,
+                                           max_seq_len_hint, status, stream)
+    if rc:
+        raise PagedAttentionError("pa_decode_q8", rc)
     return out
 
 

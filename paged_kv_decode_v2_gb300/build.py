@@ -1,10 +1,12 @@
-"""Build libpa_decode.so in-tree: nvcc for sm_103a, one object per .cu in parallel."""
+"""Build in-tree: libpa_decode.so, nvcc for sm_103a, one object per .cu in parallel; and
+_bind.so, the compiled binding of the operators that serving loops call per token."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -12,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_decode.so")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -41,8 +44,38 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_bind(force: bool) -> str:
+    """csrc/pa_bind.cpp -> an object named after the torch it is compiled against."""
+    import torch
+    src = os.path.join(CSRC, "pa_bind.cpp")
+    obj = os.path.join(BUILD, f"pa_bind-{torch.__version__}.o")
+    if force or _stale(obj, [src] + _headers()):
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+              "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+              "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj], "g++")
+    return obj
+
+
+def _link_bind(obj: str):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpa_decode.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "link of _bind.so")
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every csrc/*.cu and link libpa_decode.so; returns its path."""
+    """Compile csrc, link libpa_decode.so and _bind.so; returns the former's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     headers = _headers()
@@ -60,9 +93,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return o
 
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=min(len(todo), os.cpu_count() or 4)) as ex:
-            list(ex.map(compile_one, todo))
+    with cf.ThreadPoolExecutor(max_workers=min(len(todo), os.cpu_count() or 4) + 1) as ex:
+        bind = ex.submit(_compile_bind, force)
+        list(ex.map(compile_one, todo))
+        bind_obj = bind.result()
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -70,6 +104,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or _stale(BIND, [bind_obj]):
+        _link_bind(bind_obj)
     return LIB
 
 

@@ -51,6 +51,18 @@ def test_binding_refuses(cuda_lib):
         cuda_lib.pa_decode_q8(q.float(), kc, vc, ks, vs, tables, lens, 0.125, 64, q.float(), None, None, None)
 
 
+def test_binding_refuses_what_is_no_tensor(cuda_lib):
+    kc, vc, ks, vs, tables, lens = cu.cache8([40, 3])
+    q = torch.zeros((2, 4, 64), dtype=F16)
+    for args in ((None, kc, vc, ks, vs, tables, lens, 0.125, 64, q), (q, kc, vc, None, vs, tables, lens, 0.125, 64, q),
+                 (q, kc, vc, ks, vs, tables, [40, 3], 0.125, 64, q), (q, kc, vc, ks, vs, tables, lens, "x", 64, q),
+                 (q, kc, vc, ks, vs, tables, lens, 0.125, 6.5, q)):
+        with pytest.raises(TypeError):
+            cuda_lib.pa_decode_q8(*args, None, None, None)
+    with pytest.raises(ValueError):
+        cuda_lib.pa_decode_q8(q, kc, vc, ks, vs, tables, lens, 0.125, 2 ** 40, q, None, None, None)
+
+
 # ---------------------------------------------------------------- on the GPU
 
 gpu = pytest.mark.gpu
@@ -230,6 +242,26 @@ def test_same_bits_every_time_and_under_a_graph(pa, Q, G):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@gpu
+def test_binding_refuses_shapes(pa):
+    kc, vc, ks, vs, tables, lens = [x.cuda() for x in cu.cache8([40, 3])]
+    q = torch.zeros((2, 8, 64), dtype=F16, device="cuda")
+    out = torch.empty_like(q)
+    work = pa.alloc_workspace(2, 8, 64, 2)
+    good = dict(query=q, key_cache=kc, value_cache=vc, k_scales=ks, v_scales=vs, block_tables=tables, seq_lens=lens,
+                scale=0.125, partition_size=64, out=out, tmp_output=work[0], exp_sums=work[1], max_logits=work[2])
+    pa.pa_decode_q8(**good)
+    wrong = [("query", q[:1]), ("query", q[..., :32]), ("query", q.transpose(0, 1)), ("query", q.bfloat16()), ("out", out[:, :4]),
+             ("out", out.bfloat16()), ("key_cache", kc[:1]), ("key_cache", kc.view(torch.uint8)), ("value_cache", vc.transpose(1, 2)),
+             ("k_scales", ks[:1]), ("k_scales", ks.double()), ("v_scales", vs.t()), ("block_tables", tables.long()),
+             ("block_tables", tables[:1]), ("seq_lens", lens.cpu()), ("seq_lens", lens[:0]), ("exp_sums", None),
+             ("exp_sums", work[1].flatten()[:3]), ("max_logits", work[2].half()), ("status", lens.long()), ("status", lens[:0])]
+    for name, value in wrong:
+        with pytest.raises((TypeError, ValueError)):
+            pa.pa_decode_q8(**dict(good, **{name: value}))
+    torch.cuda.synchronize()
 
 
 @gpu

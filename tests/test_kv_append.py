@@ -334,3 +334,26 @@ def test_graph_replay_and_stream(pa):
                        other.k_scales, other.v_scales, cos_sin=other.cos_sin, token_starts=other.starts, stream=side)
     side.synchronize()
     assert torch.equal(other.key_cache.view(torch.uint8).cpu(), want[1].view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+def test_binding_refuses_shapes(pa, q8):
+    d = cu.batch([2, 1], [3, 0]).cuda()
+    out = torch.empty_like(d.query)
+    good = dict(key=d.key, value=d.value, block_tables=d.tables, seq_lens=d.lens, key_cache=d.key_cache, value_cache=d.value_cache,
+                cos_sin=d.cos_sin, query=d.query, query_out=out, token_starts=d.starts)
+    wrong = [("key", d.key[:2]), ("key", d.key[..., :32]), ("key", d.key[:, :1]), ("key", d.key.transpose(1, 2)), ("value", d.value.float()),
+             ("value", d.value[0]), ("query", None), ("query_out", None), ("query", d.query[:1]), ("query_out", out[:, :1]),
+             ("token_starts", d.starts[:2]), ("token_starts", d.starts.long()), ("token_starts", None), ("cos_sin", d.cos_sin.double()),
+             ("cos_sin", d.cos_sin[0]), ("cos_sin", d.cos_sin.t()), ("seq_lens", d.lens.cpu()), ("key_cache", d.key_cache.double()),
+             ("status", d.lens.long())]
+    if q8:
+        good.update(k_scales=d.k_scales, v_scales=d.v_scales)
+        wrong += [("k_scales", d.k_scales[:1]), ("v_scales", d.v_scales.double()), ("k_scales", None)]
+    before = d.key_cache.clone()
+    for name, value in wrong:
+        with pytest.raises((TypeError, ValueError)):
+            (pa.pa_kv_append_q8 if q8 else pa.pa_kv_append)(**dict(good, **{name: value}))
+    torch.cuda.synchronize()
+    assert torch.equal(d.key_cache.view(torch.uint8), before.view(torch.uint8))

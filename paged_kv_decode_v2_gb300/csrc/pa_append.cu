@@ -27,6 +27,8 @@
 // CTA and no two CTAs write one scale.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_q8.h"
 
@@ -316,14 +318,11 @@ __device__ __forceinline__ float scale_of(float amax)
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Four values -> four e4m3 codes; a non-finite value becomes e4m3's NaN.
+// Four values -> four e4m3 codes (NaN stays NaN; infinities saturate).
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
 {
-    auto clean = [](float x) { return fabsf(x) <= 3.4028234663852886e38f ? x : NAN; };
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(clean(a), clean(b)), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(clean(c), clean(d)), __NV_SATFINITE,
-                                                 __NV_E4M3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
 
@@ -346,13 +345,35 @@ __device__ __forceinline__ void from_e4m3x8(uint2 v, float (&x)[8])
     }
 }
 
-// Largest finite magnitude.
+// Largest magnitude; NaN when there is one.
 __device__ __forceinline__ float amax8(const float (&x)[8], float m)
 {
 #pragma unroll
+    for (int k = 0; k < 8; k += 2)
+        asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x[k]), "f"(x[k + 1]));
+    return m;
+}
+
+// The same of eight 16-bit values, as the bits of the widened value's magnitude, larger
+// than any finite one's for infinities and NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t amax8_bits(const uint4 &v, uint32_t m)
+{
+    m = __vmaxu2(m, v.x & 0x7fff7fffu);
+    m = __vmaxu2(m, v.y & 0x7fff7fffu);
+    m = __vmaxu2(m, v.z & 0x7fff7fffu);
+    return __vmaxu2(m, v.w & 0x7fff7fffu);
+}
+
+// Values that are not finite -> NaN; the largest magnitude of the others.
+__device__ __forceinline__ float clean8(float (&x)[8], float m)
+{
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float a = fabsf(x[k]);
-        m = a <= 3.4028234663852886e38f ? fmaxf(m, a) : m;
+        if (fabsf(x[k]) <= 3.4028234663852886e38f)
+            m = fmaxf(m, fabsf(x[k]));
+        else
+            x[k] = NAN;
     }
     return m;
 }
@@ -381,20 +402,21 @@ __device__ __forceinline__ void requantise(uint2 *at, float old, float now)
 
 // One CTA per item and `heads` KV heads, block_size * head_dim / 16 threads: thread
 // = (row of the block, pair of chunks).  CTAs past those rotate one token's query
-// rows each.  Several heads a CTA save the chain of loads that finds the block (and
-// the angles): prompts run 8 at a time, single tokens one, so that their CTAs fill
-// the GPU (see launch_append_q8).
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
-    append_q8_kernel(const AppendParams p, int kv_ctas, int heads)
+// rows each.  Several heads a CTA (MANY) save the chain of loads that finds the block
+// (and the angles): prompts run 8 at a time, the next head's rows loaded while this
+// one's maxima are found; few tokens one head, so that their CTAs fill the GPU (see
+// launch_append_q8).
+template <typename T, bool WIDE, bool MANY>
+__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : MANY ? 3 : 4)
+    append_q8_kernel(const AppendParams p, int kv_ctas, int heads, int block_shift, int item_shift)
 {
+    using E = Elem<T>;
     __shared__ float s_max[2][64];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
-    const int items = p.head_dim / 16;
-    const int u = threadIdx.x % items;
-    const int row = threadIdx.x / items;
+    const int u = threadIdx.x & ((1 << item_shift) - 1);
+    const int row = threadIdx.x >> item_shift;
     const bool interleaved = p.interleaved != 0;
     const Item rot = item_of(u, p.rotary_dim, interleaved, true);
     const int chunks = p.head_dim / 8;
@@ -407,7 +429,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
                                                          t * p.query_stride);
         uint4 *qo = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) +
                                               t * p.query_out_stride);
-        const int step = blockDim.x / items;
+        const int step = blockDim.x >> item_shift;
         bool placed = false;
         for (int base = row; base - row < p.num_heads; base += 2 * step) {
             uint4 x0[2], x1[2];
@@ -429,27 +451,33 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (base + i * step < p.num_heads) {
-                    float a[8], d[8];
-                    unpack8<T>(x0[i], a);
-                    unpack8<T>(x1[i], d);
-                    rotate_item(a, d, rot, interleaved, c, s);
-                    qo[(base + i * step) * chunks + rot.c0] = pack8<T>(a);
-                    qo[(base + i * step) * chunks + rot.c1] = pack8<T>(d);
+                    if (rot.rot0 || rot.rot1) {
+                        float a[8], d[8];
+                        unpack8<T>(x0[i], a);
+                        unpack8<T>(x1[i], d);
+                        rotate_item(a, d, rot, interleaved, c, s);
+                        x0[i] = pack8<T>(a);
+                        x1[i] = pack8<T>(d);
+                    }
+                    qo[(base + i * step) * chunks + rot.c0] = x0[i];
+                    qo[(base + i * step) * chunks + rot.c1] = x1[i];
                 }
         }
         return;
     }
 
     // ---- one block of `heads` KV heads, one after another
-    const int splits = (p.num_kv_heads + heads - 1) / heads;
+    const int splits = MANY ? (p.num_kv_heads + heads - 1) / heads : p.num_kv_heads;
     const int item = blockIdx.x / splits;
-    const int kv0 = ((int)blockIdx.x - item * splits) * heads;
-    const int kv1 = min(kv0 + heads, p.num_kv_heads);
-    const int bs = p.block_size;
+    const int kv0 = ((int)blockIdx.x - item * splits) * (MANY ? heads : 1);
+    const int kv1 = MANY ? min(kv0 + heads, p.num_kv_heads) : kv0 + 1;
+    const int bs = 1 << block_shift;
     Seq q;
     int j;
     if (p.token_starts) {
-        auto first_item = [&](int i, int start) { return (long long)start / bs + 2LL * i; };
+        auto first_item = [&](int i, int start) { // (as start / bs + 2 i, for any start)
+            return (long long)(start < 0 ? -(-start >> block_shift) : start >> block_shift) + 2LL * i;
+        };
         if (!find_seq(p, item, lane, first_item, q))
             return;
         j = item - (int)first_item(q.b, q.begin);
@@ -470,28 +498,29 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
             set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
         return;
     }
+    // Positions fit 32 bits (a table's do), end - begin is at most num_tokens.
     const int L = q.len;
+    const int cap = p.max_blocks << block_shift;
     const long long first = (long long)L - (end - begin); // position of the first new token
-    const long long cap = (long long)p.max_blocks * bs;
     if (first < 0 || L > cap) {
         if (reporter && j == 0)
             set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
     }
     // Positions written: from `first` (0 when negative) up to L, the table's
     // and the rotation table's ends.
-    const long long lo_pos = first < 0 ? 0 : first;
-    long long hi_pos = L < cap ? L : cap;
+    const int lo_pos = first < 0 ? 0 : (int)first;
+    int hi_pos = min(L, cap);
     if (p.rotary_dim && hi_pos > p.max_positions) {
         if (reporter && j == 0)
             set_status(p.status, PA_STATUS_BAD_POSITION);
         hi_pos = p.max_positions;
     }
-    const long long blk = lo_pos / bs + j; // logical block
-    const long long p0 = blk * bs;         // its first position
-    if (p0 >= hi_pos)
+    const int blk = (lo_pos >> block_shift) + j; // logical block
+    if (lo_pos >= hi_pos || blk > (hi_pos - 1) >> block_shift)
         return;
-    const int new_lo = (int)(lo_pos > p0 ? lo_pos - p0 : 0); // rows [new_lo, new_hi) are new
-    const int new_hi = (int)(hi_pos - p0 < bs ? hi_pos - p0 : bs);
+    const int p0 = blk << block_shift;           // its first position
+    const int new_lo = max(lo_pos - p0, 0);      // rows [new_lo, new_hi) are new
+    const int new_hi = min(hi_pos - p0, bs);
     const int32_t block = __ldg(p.block_tables + (size_t)b * p.max_blocks + blk);
     if (block < 0 || block >= p.num_blocks) {
         if (reporter)
@@ -500,19 +529,19 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
     }
     const bool is_new = row >= new_lo && row < new_hi;
     const size_t slot0 = (size_t)block * p.num_kv_heads;
-    // This thread's two chunks of K and of V; the next head's are loaded while this
-    // one's maxima are found.
+    // This thread's two chunks of K and of V.
     const Item raw = item_of(u, 0, false, false);
     const uint4 *ksrc = nullptr, *vsrc = nullptr;
     uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
     if (is_new) {
         const int t = begin + (int)(p0 + row - first);
-        ksrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) + t * p.key_stride);
-        vsrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) + t * p.value_stride);
-        k0 = __ldcs(ksrc + kv0 * chunks + rot.c0);
-        k1 = __ldcs(ksrc + kv0 * chunks + rot.c1);
-        v0 = __ldcs(vsrc + kv0 * chunks + raw.c0);
-        v1 = __ldcs(vsrc + kv0 * chunks + raw.c1);
+        ksrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) + t * p.key_stride) + kv0 * chunks;
+        vsrc = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) + t * p.value_stride) +
+               kv0 * chunks;
+        k0 = __ldcs(ksrc + rot.c0);
+        k1 = __ldcs(ksrc + rot.c1);
+        v0 = __ldcs(vsrc + raw.c0);
+        v1 = __ldcs(vsrc + raw.c1);
         if (p.rotary_dim)
             load_angles(p.cos_sin + (size_t)(p0 + row) * p.rotary_dim, rot, p.rotary_dim,
                         interleaved, c, s);
@@ -526,54 +555,61 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3)
         float a[8], d[8];
         unpack8<T>(k0, a);
         unpack8<T>(k1, d);
-        rotate_item(a, d, rot, interleaved, c, s);
+        if (rot.rot0 || rot.rot1)
+            rotate_item(a, d, rot, interleaved, c, s);
         const uint4 w0 = v0, w1 = v1;
-        if (is_new && kv + 1 < kv1) {
-            k0 = __ldcs(ksrc + (kv + 1) * chunks + rot.c0);
-            k1 = __ldcs(ksrc + (kv + 1) * chunks + rot.c1);
-            v0 = __ldcs(vsrc + (kv + 1) * chunks + raw.c0);
-            v1 = __ldcs(vsrc + (kv + 1) * chunks + raw.c1);
+        if (MANY && is_new && kv + 1 < kv1) {
+            ksrc += chunks;
+            vsrc += chunks;
+            k0 = __ldcs(ksrc + rot.c0);
+            k1 = __ldcs(ksrc + rot.c1);
+            v0 = __ldcs(vsrc + raw.c0);
+            v1 = __ldcs(vsrc + raw.c1);
         }
-        float mk = amax8(d, amax8(a, 0.f)), mv;
-        {
-            float x[8];
-            unpack8<T>(w0, x);
-            mv = amax8(x, 0.f);
-            unpack8<T>(w1, x);
-            mv = amax8(x, mv);
-        }
-        // Non-negative floats order as their bits.
-        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
-        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+        float mk = amax8(d, amax8(a, 0.f));
+        const uint32_t vb = amax8_bits<T>(w1, amax8_bits<T>(w0, 0u));
+        // (an infinity or NaN widens to one)
+        float mv = E::lo(max(vb & 0xffffu, vb >> 16));
         float *const sm = s_max[kv & 1]; // the head before may still be reading the other half
-        if (lane == 0) {
-            sm[threadIdx.x >> 5] = mk;
-            sm[32 + (threadIdx.x >> 5)] = mv;
+        // The CTA's maxima; magnitudes order as their bits, NaN last.
+        auto over_cta = [&]() {
+            mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mk))));
+            mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mv))));
+            if (lane == 0) {
+                sm[threadIdx.x >> 5] = mk;
+                sm[32 + (threadIdx.x >> 5)] = mv;
+            }
+            __syncthreads();
+            mk = lane < warps ? sm[lane] : 0.f;
+            mv = lane < warps ? sm[32 + lane] : 0.f;
+            mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+            mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+        };
+        over_cta();
+        float x[8], y[8];
+        unpack8<T>(w0, x);
+        unpack8<T>(w1, y);
+        if (!(mk <= 3.4028234663852886e38f && mv <= 3.4028234663852886e38f)) {
+            // Some value is not finite: it becomes e4m3's NaN, beside the scale of the others.
+            mk = clean8(d, clean8(a, 0.f));
+            mv = clean8(y, clean8(x, 0.f));
+            __syncthreads(); // everyone has read the maxima
+            over_cta();
         }
-        __syncthreads();
-        mk = lane < warps ? sm[lane] : 0.f;
-        mv = lane < warps ? sm[32 + lane] : 0.f;
-        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
-        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
         const float sk = fmaxf(scale_of(mk), old_k), sv = fmaxf(scale_of(mv), old_v);
         if (threadIdx.x == 0) {
             p.k_scales[slot] = sk;
             p.v_scales[slot] = sv;
         }
-        uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) +
-                                              (slot * bs + row) * p.head_dim);
-        uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) +
-                                              (slot * bs + row) * p.head_dim);
+        const size_t at = ((slot << block_shift) + row) * p.head_dim;
+        uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) + at);
+        uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) + at);
         if (is_new) {
             // x / s is x times an exact power of two for the scales this writes.
             const float fk = 1.f / sk, fv = 1.f / sv;
             kd[rot.c0] = to_e4m3x8(a, fk);
             kd[rot.c1] = to_e4m3x8(d, fk);
-            float x[8];
-            unpack8<T>(w0, x);
-            const uint2 e = to_e4m3x8(x, fv);
-            unpack8<T>(w1, x);
-            const uint2 f = to_e4m3x8(x, fv);
+            const uint2 e = to_e4m3x8(x, fv), f = to_e4m3x8(y, fv);
             *reinterpret_cast<uint4 *>(vd + raw.c0) = make_uint4(e.x, e.y, f.x, f.y);
         } else if (row < new_lo) {
             requantise(kd + raw.c0, old_k, sk);
@@ -622,6 +658,14 @@ long long append_q8_ctas(const AppendParams &p)
 constexpr int kMaxHeads = 8;     // KV heads of a CTA at most
 constexpr int kApartTokens = 60; // tokens per SM from which queries get their own launch
 
+static int log2_of(int x) // of a power of two
+{
+    int n = 0;
+    while (1 << n < x)
+        ++n;
+    return n;
+}
+
 cudaError_t launch_append_q8(int dtype, const AppendParams &p, int num_sms, cudaStream_t stream)
 {
     // KV heads of a CTA: as many as leave some eight CTAs per SM (counting the items
@@ -636,18 +680,20 @@ cudaError_t launch_append_q8(int dtype, const AppendParams &p, int num_sms, cuda
     // flight); few share this launch.
     const bool apart = p.num_heads && p.num_tokens >= kApartTokens * num_sms;
     int kv_ctas = (int)(items * splits);
-    void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas, &heads};
+    int block_shift = log2_of(p.block_size), item_shift = log2_of(p.head_dim / 16);
+    void *args[] = {const_cast<AppendParams *>(&p), &kv_ctas, &heads, &block_shift, &item_shift};
     const unsigned threads = (unsigned)(p.block_size * p.head_dim / 16);
     const unsigned grid = (unsigned)(kv_ctas + (p.num_heads && !apart ? p.num_tokens : 0));
-    cudaError_t e;
-    if (threads <= 256)
-        e = dtype == PA_BF16
-                ? launch_pdl(&append_q8_kernel<__nv_bfloat16, false>, grid, threads, stream, args)
-                : launch_pdl(&append_q8_kernel<__half, false>, grid, threads, stream, args);
-    else
-        e = dtype == PA_BF16
-                ? launch_pdl(&append_q8_kernel<__nv_bfloat16, true>, grid, threads, stream, args)
-                : launch_pdl(&append_q8_kernel<__half, true>, grid, threads, stream, args);
+    auto launch = [&](auto wide, auto many) {
+        return dtype == PA_BF16
+                   ? launch_pdl(&append_q8_kernel<__nv_bfloat16, wide.value, many.value>, grid, threads, stream, args)
+                   : launch_pdl(&append_q8_kernel<__half, wide.value, many.value>, grid, threads, stream, args);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    const cudaError_t e = threads <= 256 ? heads > 1 ? launch(no, yes) : launch(no, no)
+                          : heads > 1    ? launch(yes, yes)
+                                         : launch(yes, no);
     if (e != cudaSuccess || !apart)
         return e;
     AppendParams q = p;

@@ -102,6 +102,9 @@ struct Q8Params {
     int seq_len_cap;
     float scale;
     int partition_size;          // V2, and V1 over a cluster: tokens of a CTA
+    int num_seqs;
+    int num_parts;               // V2: partitions per sequence
+    int sorted;                  // units by size (at most kQ8Sorted sequences)
     int ways;                    // V1: CTAs of a cluster that share a row tile's tokens
     int stages;                  // K ring stages
     int v_stages;                // V ring stages
@@ -145,6 +148,7 @@ struct Q8Launch {
 
 // The tcgen05 kernels: one per (head_dim, rows per CTA), see pa_q8_tc.cuh.
 constexpr int kQ8Tok = 128; // tokens per tile
+constexpr int kQ8Sorted = 256; // sequences that a CTA's threads sort
 constexpr int kQ8Ways = 8;  // CTAs of a cluster at most (the portable size)
 struct Q8TcKernel {
     const void *fn;

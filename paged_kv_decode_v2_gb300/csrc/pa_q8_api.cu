@@ -26,7 +26,10 @@ int rows_per_cta(int cols, int head_dim)
     return cols <= 32 || head_dim == 256 ? 32 : 64;
 }
 
-std::atomic<int> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
+// CTAs of the kernel that share an SM.
+int ctas_per_sm(int nr, int head_dim) { return nr <= 32 && head_dim <= 128 ? 2 : 1; }
+
+std::atomic<int64_t> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
 
 int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
 {
@@ -35,10 +38,10 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
         return PA_ERR_UNSUPPORTED;
     const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
     const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
-    std::atomic<int> &cell =
+    std::atomic<int64_t> &cell =
         g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
-    // Dynamic limit after the opt-in in the low 18 bits, static bytes above them.
-    int have = cell.load(std::memory_order_acquire);
+    // Dynamic limit after the opt-in in the low half, static bytes above.
+    int64_t have = cell.load(std::memory_order_acquire);
     if (have == 0) {
         int optin = 0;
         cudaFuncAttributes fa;
@@ -46,13 +49,12 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
             cudaFuncGetAttributes(&fa, k.fn) != cudaSuccess || (size_t)optin <= fa.sharedSizeBytes)
             return PA_ERR_CUDA;
         const int dyn = optin - (int)fa.sharedSizeBytes;
-        if (dyn >= 1 << 18 ||
-            cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+        if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
             return PA_ERR_CUDA;
-        have = dyn | (int)fa.sharedSizeBytes << 18;
+        have = dyn | (int64_t)fa.sharedSizeBytes << 32;
         cell.store(have, std::memory_order_release);
     }
-    const size_t limit = have & 0x3ffff, fixed_static = have >> 18;
+    const size_t limit = have & 0xffffffff, fixed_static = have >> 32;
     const size_t tile = (size_t)kQ8Tok * L.head_dim;
     int tune_w, tune_s, rows_kernel;
     host_tuning(&tune_w, &tune_s, &rows_kernel);
@@ -248,13 +250,14 @@ struct Q8Cut {
     int part, ways, per;
 };
 
-// A CTA costs some 5 us beside its tiles, so partitions are long: as many per group
-// as make one wave of CTAs, where that takes at most kWavePart tokens each (one
-// sequence of 100,000 tokens, 4 KV heads: 1408 tokens 21.4 us, 2048 22.7, 1024 27.2);
-// else kMaxPart if those are three waves or more, so that lengths even out, else
-// kWavePart (64 sequences of up to 32,768: 4096 89 us, 2048 100, 8192 95; 32 of up
-// to 8192: 2048 56 us, 1024 60, 4096 62).
-constexpr int kWavePart = 2048, kMaxPart = 4096;
+// A CTA costs some 5 us beside its tiles, so partitions are long.  One wave of CTAs
+// (as many partitions per group as give every place a CTA) if that takes at most
+// kWavePart tokens each: one sequence of 100,000 tokens, 4 KV heads: 1408 tokens 21.4
+// us, 2048 22.7, 1024 27.2.  Else two waves or more, sorted by size (see the kernel),
+// the fewest whose partitions have at most kMaxPart tokens: 32 sequences of up to 8192,
+// 8 KV heads: 4096 53 us, 2048 55, 8192 60; 64 of up to 32,768: 8192 76 us, 4096 85,
+// 16,384 112; 16 new tokens for 32 of up to 8192: 8192 93 us, 4096 104.
+constexpr int kWavePart = 2048, kMaxPart = 8192;
 // V1 unless a CTA of its cluster has more tiles than a partition by more than this:
 // what the second launch costs (8 groups of 8000 tokens: V2 10.5 us at 4 tiles, V1
 // 12.9 at 8; of 4000 tokens both 4 tiles, 9.9 us in either).
@@ -266,7 +269,7 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
     const int nr = rows_per_cta(q_len * group, head_dim);
     const long long groups = (long long)num_seqs * num_kv_heads * row_groups(q_len * group, head_dim);
     const long long tiles = ((long long)max_seq_len + kQ8Tok - 1) / kQ8Tok;
-    const long long slots = (long long)sms * (nr <= 32 && head_dim <= 128 ? 2 : 1);
+    const long long slots = (long long)sms * ctas_per_sm(nr, head_dim);
     Q8Cut cut = {0, 1, 0};
     if (tiles <= 1)
         return cut;
@@ -274,11 +277,17 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
     const long long per = (tiles + ways - 1) / ways;
     cut.ways = (int)((tiles + per - 1) / per);
     cut.per = (int)std::min(per * kQ8Tok, (long long)INT32_MAX);
-    const long long wave = std::max(1LL, slots / groups); // partitions per group in one wave
-    long long part = (tiles + wave - 1) / wave * kQ8Tok;
+    auto in_waves = [&](long long k) { // tokens of a partition, k waves
+        const long long np = std::max(1LL, k * slots / groups);
+        return (tiles + np - 1) / np * kQ8Tok;
+    };
+    long long part = in_waves(1);
     if (part > kWavePart) {
-        const long long np = ((long long)max_seq_len + kMaxPart - 1) / kMaxPart;
-        part = groups * np >= 3 * slots ? kMaxPart : kWavePart;
+        part = in_waves(2);
+        if (part > kMaxPart) {
+            const long long np = (max_seq_len + kMaxPart - 1LL) / kMaxPart; // at least
+            part = in_waves((np * groups + slots - 1) / slots);
+        }
     }
     part = std::max(part, (long long)partition_size);
     if (part < max_seq_len && per > (part + kQ8Tok - 1) / kQ8Tok + kJoinTiles)
@@ -480,7 +489,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.seq_len_cap = cap;
     p.scale = scale;
     p.partition_size = part ? part : cut.per;
-    p.ways = cut.ways;
+    p.ways = part ? 1 : cut.ways;
     p.max_num_partitions = max_num_partitions;
     p.tmp_output = tmp_output;
     p.exp_sums = exp_sums;
@@ -512,11 +521,15 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
             p.ways = 1;
         }
     }
-    // Column groups of one partition are adjacent in x: their reads meet in L2.
-    const long long gx = (long long)(L.v1 ? p.ways : np) * p.col_groups;
+    const long long gx = (long long)num_seqs * num_kv_heads * p.col_groups * (L.v1 ? p.ways : np);
     if (gx > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    L.grid = dim3((unsigned)gx, num_kv_heads, num_seqs);
+    L.grid = dim3((unsigned)gx);
+    // By size where CTAs wait for their turn (the sort costs each some 0.4 us).
+    p.num_seqs = num_seqs;
+    p.num_parts = np;
+    p.sorted = num_seqs > 1 && num_seqs <= kQ8Sorted && p.ways == 1 &&
+               gx > (long long)sms * ctas_per_sm(rows_per_cta(p.cols, head_dim), head_dim);
     rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);
     if (rc || L.v1)
         return rc;

@@ -43,7 +43,7 @@
 //
 // Warp roles: warpgroups of softmax warps (16 rows each at most; thread = token
 // = TMEM lane, and dim in the epilogue), one warp that issues the MMAs of S (and
-// owns the tensor memory), one that issues those of P.V, four that issue the TMA loads (half a K or V tile each).
+// owns the tensor memory), one that issues those of P.V, two or four that issue the TMA loads.
 // S and P have two buffers where tensor memory allows (else one): S of tile
 // t + 2 is issued once the softmax has read S of tile t.
 #pragma once
@@ -63,8 +63,6 @@ constexpr float kQ8NoMax = -1e30f; // M before a row has seen a token
 constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4,
 constexpr float kQ8Unit = 11.f;    // stored times 2^11: <= 2^15 (e5m2's largest is 1.75 * 2^15)
 constexpr float kQ8Floor = -60.f;  // of log2(vs / r)
-constexpr int kQ8Load = 4;         // producer warps: two for K, two for V
-constexpr int kQ8Chap = 512;       // blocks whose scales are held in shared memory at a time
 
 // ---------------------------------------------------------------- primitives
 
@@ -312,16 +310,22 @@ struct Q8Cfg {
     static constexpr uint32_t kQBytes = kSN * D;
     static constexpr int kRW = NR < 16 ? NR : 16;                 // rows of a softmax warpgroup
     static constexpr int kWG = NR / kRW;
-    static_assert(kWG * 128 <= kQ8Chap, "a thread holds one block of the first chapter");
+    static constexpr int kChap = kWG * 128 < 256 ? 256 : kWG * 128; // blocks whose scales are held at a time
     static constexpr int kSoft = kWG * 128;
-    static constexpr int kThreads = kSoft + 64 + 32 * kQ8Load;
+    // Producer warps: two for K and two for V, or one each from 16 rows on, where a tile
+    // lasts longer and the softmax warps want the registers (16 new tokens: 121 ->
+    // 104 us; one each at 8 rows: 100k tokens 22.0 -> 22.7, batches the same).
+    static constexpr int kLoad = NR <= 8 ? 4 : 2;
+    static constexpr int kThreads = kSoft + 64 + 32 * kLoad;
     static constexpr int kMinCtas = D > 128 ? 1 : NR <= 32 ? 2 : 1;
     static constexpr int kCtas = kMinCtas * (int)kCols <= 512 ? kMinCtas : 512 / (int)kCols;
     static constexpr uint32_t kFixed = 1024 + kBuf * kPBytes + kQBytes;
 };
 
+// (Registers are handed out to warps by fours: launch bounds of a multiple of 128
+// threads let two CTAs share an SM.)
 template <int D, int NR, int PL, bool V1>
-__global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::kMinCtas)
+__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
 {
@@ -345,20 +349,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     __shared__ int s_red[C::kSoft / 32][kRW];
     __shared__ float s_part[C::kSoft / 32][kRW];
     __shared__ float s_vref[C::kSoft / 32];
-    __shared__ float s_ks[kQ8Chap], s_lv[kQ8Chap], s_rl[kQ8Chap]; // a chapter's ks, lv, 2^-lv
+    __shared__ float s_ks[C::kChap], s_lv[C::kChap], s_rl[C::kChap]; // a chapter's ks, lv, 2^-lv
     extern __shared__ uint8_t dyn_smem[];
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    // blockIdx.x = partition * col_groups + row tile; V1: row tile * ways + rank, the
-    // `ways` CTAs of a cluster a row tile's partitions.
-    const bool one_group = p.col_groups == 1;
-    const int ways = V1 ? p.ways : 1;
-    const int rt = V1 ? (int)blockIdx.x / ways : one_group ? 0 : (int)blockIdx.x % p.col_groups;
-    const int part = V1 ? (int)blockIdx.x % ways : one_group ? (int)blockIdx.x : (int)blockIdx.x / p.col_groups;
-    const int kv = blockIdx.y;
-    const int b = blockIdx.z;
-
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
@@ -370,6 +365,98 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     if (p.only_if && __ldcg(p.only_if) == 0)
         return;
 
+    // blockIdx.x = ((unit * KV + KV head) * row tiles + row tile) * ways + rank: units are
+    // partitions of sequences (V1: sequences, the `ways` CTAs of a cluster their
+    // partitions); row tiles of one KV head are neighbours, so that their reads meet
+    // in L2.
+    const int ways = V1 ? p.ways : 1;
+    int unit = V1 ? (int)blockIdx.x / ways : (int)blockIdx.x;
+    int part = V1 ? (int)blockIdx.x % ways : 0;
+    int rt = 0;
+    if (p.col_groups > 1) {
+        rt = unit % p.col_groups;
+        unit /= p.col_groups;
+    }
+    const int kv = unit % p.num_kv_heads;
+    unit /= p.num_kv_heads;
+    const bool reporter = kv == 0 && rt == 0 && (!V1 || part == 0);
+    auto length = [&](int at, bool report) -> int {
+        const int len = __ldg(p.seq_lens + at);
+        if (len >= 0 && len <= p.seq_len_cap)
+            return len;
+        if (report)
+            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
+        return len < 0 ? 0 : p.seq_len_cap;
+    };
+    int b, L;
+    if (p.sorted) {
+        // Units by the tokens they hold, whole partitions first, then the rest of each
+        // sequence (V1: each sequence) in 32 classes of size, so that no long one is
+        // left for the end.  Every CTA sorts: thread = sequence.
+        constexpr int kWarps = C::kThreads / 32;
+        __shared__ int s_count[kWarps][32]; // sequences of each class, by warp
+        __shared__ int s_whole[kWarps];     // whole partitions
+        __shared__ int s_pick[3];
+        const int at = threadIdx.x;
+        const int len = at < p.num_seqs ? length(at, reporter && unit == 0) : 0;
+        const int size = V1 ? p.seq_len_cap : p.partition_size;
+        const int whole = V1 ? 0 : len / size;
+        const int rest = len - whole * size;
+        int cls = -1; // 0 (largest) to 31; none without a unit
+        if (V1 ? at < p.num_seqs : rest > 0)
+            cls = (int)((long long)(size - rest) * 32 / (size + 1LL));
+        s_count[warp][lane] = 0;
+        if (threadIdx.x == 0)
+            s_pick[0] = -1;
+        __syncwarp();
+        const uint32_t peers = __match_any_sync(0xffffffffu, cls);
+        const int ahead = __popc(peers & ((1u << lane) - 1u));
+        if (cls >= 0 && ahead == 0)
+            s_count[warp][cls] = __popc(peers);
+        int run = whole; // inclusive scan
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, off);
+            run += lane >= off ? v : 0;
+        }
+        if (lane == 31)
+            s_whole[warp] = run;
+        __syncthreads();
+        const int used = (p.num_seqs + 31) / 32; // warps that hold sequences
+        int total = 0, start = run - whole, count = 0, before = 0;
+        for (int w = 0; w < used; ++w) {
+            const int n = s_whole[w], c = s_count[w][lane];
+            total += n;
+            start += w < warp ? n : 0;
+            count += c;
+            before += w < warp ? c : 0;
+        }
+        int up = count; // of this lane's class and those ahead of it
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, up, off);
+            up += lane >= off ? v : 0;
+        }
+        const int first = __shfl_sync(0xffffffffu, total + up - count + before, cls & 31) + ahead;
+        const bool in_whole = unit >= start && unit - start < whole;
+        if (in_whole || (cls >= 0 && unit == first)) {
+            s_pick[0] = at;
+            s_pick[1] = in_whole ? unit - start : whole;
+            s_pick[2] = len;
+        }
+        __syncthreads();
+        b = s_pick[0];
+        if (b < 0)
+            return; // past the last unit
+        part = s_pick[1];
+        L = s_pick[2];
+    } else if (V1) {
+        b = unit;
+    } else {
+        b = unit / p.num_parts;
+        part = unit - b * p.num_parts;
+    }
+
     const int tokA = part * p.partition_size;
     const int sh = p.block_shift, bs = 1 << sh; // block size
     const int bpt = kQ8Tok >> sh;               // blocks per tile: 2 to 16
@@ -379,12 +466,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     int32_t id_first = 0;
     if (threadIdx.x < C::kSoft && blk0 + (int)threadIdx.x < p.max_blocks)
         id_first = __ldg(bt + threadIdx.x);
-    int L = __ldg(&p.seq_lens[b]);
-    if (L < 0 || L > p.seq_len_cap) {
-        if (threadIdx.x == 0 && part == 0 && kv == 0 && rt == 0)
-            set_status(p.status, PA_STATUS_BAD_SEQ_LEN);
-        L = L < 0 ? 0 : p.seq_len_cap;
-    }
+    if (!p.sorted)
+        L = length(b, reporter && part == 0 && threadIdx.x == 0);
     if (!V1 && tokA >= L)
         return; // partition past the end of the sequence: nothing to write
 
@@ -453,12 +536,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         tmem_relinquish();
     }
     int32_t status_bits = 0;
-    // Producer warp w loads half w & 1 of the blocks of every K (w < 2) or V tile.
-    // One warp issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80
-    // clocks each) would bound the loop.
+    // A producer warp loads all or half the blocks of every K or V tile: one warp
+    // issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80 clocks each)
+    // would bound the loop of few rows.
+    constexpr int kSplit = C::kLoad / 2; // producer warps of one tile
     const int pw = warp - kTmaWarp;
-    const bool is_k = pw < 2;
-    const int p_first = (pw & 1) * (bpt / 2), p_num = bpt / 2; // its blocks of a tile
+    const bool is_k = pw < kSplit;
+    const int p_num = bpt / kSplit, p_first = pw % kSplit * p_num; // its blocks of a tile
     const int p_stages = is_k ? kst : vst;
     const uint32_t p_full_bar = is_k ? b_k_full : b_v_full, p_empty_bar = is_k ? b_k_empty : b_v_empty;
     const uint32_t p_ring = is_k ? k_sm : v_sm;
@@ -490,11 +574,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     };
     if (threadIdx.x == kTmaWarp * 32) {
         for (int s = 0; s < kst; ++s) {
-            mbar_init(b_k_full + 8 * s, 2);
+            mbar_init(b_k_full + 8 * s, kSplit);
             mbar_init(b_k_empty + 8 * s, 1);
         }
         for (int s = 0; s < vst; ++s) {
-            mbar_init(b_v_full + 8 * s, 2);
+            mbar_init(b_v_full + 8 * s, kSplit);
             mbar_init(b_v_empty + 8 * s, 1);
         }
         for (int j = 0; j < 2; ++j) {
@@ -511,7 +595,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
     int32_t id_next = 0;     // this lane's block of the next one, fetched ahead of its stage
     if (warp >= kTmaWarp) {
         // The first tiles, before the rest of the set-up.
-        bar_sync(15, 32 * kQ8Load); // the barriers are initialised
+        bar_sync(15, 32 * C::kLoad); // the barriers are initialised
         id_next = fetch_id(0);
         while (issued < ntiles && issued < p_stages) {
             const int32_t id = id_next;
@@ -734,7 +818,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
             s_rl[i] = fast_exp2(-lv);
         };
         auto load_chapter = [&](int j0, int i0) { // blocks j0 + i, i >= i0
-            for (int i = i0 + threadIdx.x; i < kQ8Chap; i += C::kSoft) {
+            for (int i = i0 + threadIdx.x; i < C::kChap; i += C::kSoft) {
                 float k = 0.f, v = 0.f;
                 if (j0 + i < nblk) {
                     const size_t at = (size_t)valid_id(__ldg(bt + j0 + i)) * p.num_kv_heads + kv;
@@ -762,13 +846,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, NR, PL>::kThreads, Q8Cfg<D, NR, PL>::
         bool ok = true;
         for (int t = 0; t < ntiles; ++t) {
             const int j = C::kBuf == 2 ? t & 1 : 0;
-            if (t > 0 && (t * bpt) % kQ8Chap == 0) {
-                // The next chapter of scales (ranges of more than kQ8Chap blocks).
+            if (t > 0 && (t * bpt) % C::kChap == 0) {
+                // The next chapter of scales (ranges of more than kChap blocks).
                 bar_sync(1, C::kSoft);
                 load_chapter(t * bpt, 0);
                 bar_sync(1, C::kSoft);
             }
-            const int at = (t * bpt + (tk >> sh)) & (kQ8Chap - 1); // this token's block
+            const int at = (t * bpt + (tk >> sh)) & (C::kChap - 1); // this token's block
             const float ks = s_ks[at], lv = s_lv[at], rl = s_rl[at];
             const int first = t * kQ8Tok; // from tok0
             const bool full = first >= rel_a && first + kQ8Tok <= rel_all;

@@ -104,6 +104,8 @@ struct Q8Params {
     int partition_size;          // V2, and V1 over a cluster: tokens of a CTA
     int num_seqs;
     int num_parts;               // V2: partitions per sequence
+    uint32_t group_inv;          // ceil(2^32 / group), group > 1
+    float class_scale;           // sorted: 32 classes over a whole unit's tokens
     int sorted;                  // units by size (at most kQ8Sorted sequences)
     int ways;                    // V1: CTAs of a cluster that share a row tile's tokens
     int stages;                  // K ring stages

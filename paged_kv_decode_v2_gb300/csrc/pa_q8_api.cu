@@ -480,6 +480,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.group = group;
+    p.group_inv = group > 1 ? (uint32_t)(((1ull << 32) + group - 1) / group) : 0;
     p.q_len = q_len;
     p.cols = group * q_len;
     p.col_groups = row_groups(p.cols, head_dim);
@@ -528,6 +529,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     // By size where CTAs wait for their turn (the sort costs each some 0.4 us).
     p.num_seqs = num_seqs;
     p.num_parts = np;
+    p.class_scale = 32.f / (float)(L.v1 ? cap : part);
     p.sorted = num_seqs > 1 && num_seqs <= kQ8Sorted && p.ways == 1 &&
                gx > (long long)sms * ctas_per_sm(rows_per_cta(p.cols, head_dim), head_dim);
     rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);

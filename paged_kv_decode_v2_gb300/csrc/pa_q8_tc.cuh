@@ -177,6 +177,20 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
+// mbar_wait_abortable for a warp: true in all lanes or in none.  The loop is a function
+// of its own: a copy at every wait crowded the instruction cache (16 new tokens 91.7
+// us, 89.1 without).
+static __device__ __noinline__ bool warp_wait_loop(uint32_t bar, uint32_t parity, const volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort));
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    return warp_wait_loop(bar, parity, abort);
+}
+
 // Barrier over `count` threads (a multiple of the warp size), and one that
 // also ORs a predicate over them.
 __device__ __forceinline__ void bar_sync(int id, int count)
@@ -313,8 +327,8 @@ struct Q8Cfg {
     static constexpr int kChap = kWG * 128 < 256 ? 256 : kWG * 128; // blocks whose scales are held at a time
     static constexpr int kSoft = kWG * 128;
     // Producer warps: two for K and two for V, or one each from 16 rows on, where a tile
-    // lasts longer and the softmax warps want the registers (16 new tokens: 121 ->
-    // 104 us; one each at 8 rows: 100k tokens 22.0 -> 22.7, batches the same).
+    // lasts longer and the softmax warps want the registers (16 new tokens 104 us, 121
+    // with four; at 8 rows 100k tokens 22.0, 22.7 with two).
     static constexpr int kLoad = NR <= 8 ? 4 : 2;
     static constexpr int kThreads = kSoft + 64 + 32 * kLoad;
     static constexpr int kMinCtas = D > 128 ? 1 : NR <= 32 ? 2 : 1;
@@ -404,7 +418,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         const int rest = len - whole * size;
         int cls = -1; // 0 (largest) to 31; none without a unit
         if (V1 ? at < p.num_seqs : rest > 0)
-            cls = (int)((long long)(size - rest) * 32 / (size + 1LL));
+            cls = min((int)((float)(size - rest) * p.class_scale), 31);
         s_count[warp][lane] = 0;
         if (threadIdx.x == 0)
             s_pick[0] = -1;
@@ -474,12 +488,15 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     // Rows [c0, c0 + nrows) of the KV head's cols = q_len * group rows.
     const int c0 = rt * NR;
     const int nrows = min(NR, p.cols - c0);
-    const int i_last = p.q_len == 1 ? 0 : (c0 + nrows - 1) / p.group;
+    // c / group: c < 2^18 and group <= 64, so that the multiplier's excess stays below 1.
+    auto new_token = [&](int c) -> int {
+        return p.group == 1 ? c : (int)__umulhi((uint32_t)c, p.group_inv);
+    };
+    const int i_last = p.q_len == 1 ? 0 : new_token(c0 + nrows - 1);
     auto row_of = [&](int r) -> size_t { // row of [S * q_len * H] of local row r
         const int c = c0 + r;
-        if (p.q_len == 1)
-            return (size_t)b * p.num_heads + kv * p.group + c;
-        return ((size_t)b * p.q_len + c / p.group) * p.num_heads + kv * p.group + c % p.group;
+        const int i = p.q_len == 1 ? 0 : new_token(c);
+        return (size_t)(b * p.q_len + i) * p.num_heads + (kv * p.group + c - i * p.group);
     };
     // Tokens the CTA needs: [tokA, tokE), the range cut by the causal limit of
     // its last new token (new token i sees positions <= L - q_len + i).
@@ -685,7 +702,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         int s = 0;
         uint32_t ph = 0u;
         for (; issued < ntiles; ++issued) {
-            if (!__all_sync(0xffffffffu, mbar_wait_abortable(p_empty_bar + 8 * s, ph, abort_flag))) {
+            if (!warp_wait(p_empty_bar + 8 * s, ph, abort_flag)) {
                 status_bits |= PA_STATUS_TIMEOUT;
                 *abort_flag = 1;
                 break;
@@ -724,11 +741,10 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             const int j = C::kBuf == 2 ? t & 1 : 0;
             if (is_s) {
                 // S(t) once K tile t has landed and softmax(t - kBuf) has read the buffer.
-                ok = mbar_wait_abortable(b_k_full + 8 * s, ph, abort_flag) &&
-                     (t < C::kBuf ||
-                      mbar_wait_abortable(b_p_full + 8 * ((t - C::kBuf) & 1),
-                                          (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag));
-                if (!__all_sync(0xffffffffu, ok))
+                ok = warp_wait(b_k_full + 8 * s, ph, abort_flag) &&
+                     (t < C::kBuf || warp_wait(b_p_full + 8 * ((t - C::kBuf) & 1),
+                                               (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag));
+                if (!ok)
                     break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -752,9 +768,9 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 }
             } else {
                 // P.V(t) once P(t) is written and V tile t has landed.
-                ok = mbar_wait_abortable(b_v_full + 8 * s, ph, abort_flag) &&
-                     mbar_wait_abortable(b_p_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, ok))
+                ok = warp_wait(b_v_full + 8 * s, ph, abort_flag) &&
+                     warp_wait(b_p_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1u, abort_flag);
+                if (!ok)
                     break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -778,7 +794,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 }
             }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) {
             status_bits |= PA_STATUS_TIMEOUT;
             *abort_flag = 1;
         }
@@ -838,11 +854,17 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         // (a range is less than 2^31 - 128 tokens long: its tiles' ends fit 32 bits).
         const int rel_a = tokA - tok0, rel_e = tokE - tok0;
         const int rel_q = L - p.q_len - tok0;
-        const int rel_all = min(rel_e, rel_q + (p.q_len == 1 ? 0 : c0 / p.group) + 1);
+        const int rel_all = min(rel_e, rel_q + (p.q_len == 1 ? 0 : new_token(c0)) + 1);
+        // Tiles [full_lo, full_hi) are seen whole by every row.
+        const int full_lo = (rel_a + kQ8Tok - 1) / kQ8Tok, full_hi = rel_all < 0 ? 0 : rel_all / kQ8Tok;
         uint64_t l2[kRW / 2]; // pairs of rows
 #pragma unroll
         for (int r = 0; r < kRW / 2; ++r)
             l2[r] = 0;
+        // Where this thread's row of P begins, in the first buffer: 16-byte chunk c of a
+        // row lies where the swizzle places it; part k's chunk differs in its own bits.
+        constexpr int kPLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
+        const uint32_t prow = p_sm + tk * C::kPW + (((row0 / 16) ^ ((tk >> kPLg) & (C::kPW / 16 - 1))) << 4);
         bool ok = true;
         for (int t = 0; t < ntiles; ++t) {
             const int j = C::kBuf == 2 ? t & 1 : 0;
@@ -854,25 +876,23 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             }
             const int at = (t * bpt + (tk >> sh)) & (C::kChap - 1); // this token's block
             const float ks = s_ks[at], lv = s_lv[at], rl = s_rl[at];
-            const int first = t * kQ8Tok; // from tok0
-            const bool full = first >= rel_a && first + kQ8Tok <= rel_all;
+            const bool full = t >= full_lo && t < full_hi;
             // First visible row of this thread's token: new token i = (c0 + r) /
             // group sees it when i >= pos - (L - q_len).
             int r_min = 0;
             if (!full) {
-                const int pos = first + tk;
+                const int pos = t * kQ8Tok + tk; // from tok0
                 const int i0 = pos - rel_q;
                 const long long r0 = i0 > 0 ? (long long)i0 * p.group - c0 : 0;
                 r_min = pos < rel_a || pos >= rel_e || r0 > NR ? NR : (int)(r0 < 0 ? 0 : r0);
             }
 
-            if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (t & 1),
-                                                             (uint32_t)(t >> 1) & 1u, abort_flag)))
+            if (!warp_wait(b_s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1u, abort_flag))
                 ok = false;
             tc_fence_after();
             const uint32_t sc = lane_base + C::kSCol + (uint32_t)j * C::kSReg + row0;
             // Exponents of the stored weights, s + lv + (11 - M); with raw, s + lv.
-            float x[kRW];
+            uint64_t x[kRW / 2]; // pairs of rows
             auto exponents = [&](bool raw) -> float {
                 float top = -INFINITY;
                 uint32_t sr[PL][kRW];
@@ -898,18 +918,24 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                                        f2_pack(__uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1])));
                         const uint64_t add =
                             raw ? lv2 : f2_add(lv2, h ? f2_pack(nm.z, nm.w) : f2_pack(nm.x, nm.y));
-                        f2_unpack(f2_fma(s, f2_mul(ks2, h ? f2_pack(cf.z, cf.w) : f2_pack(cf.x, cf.y)), add),
-                                  x[i], x[i + 1]);
+                        x[i / 2] = f2_fma(s, f2_mul(ks2, h ? f2_pack(cf.z, cf.w) : f2_pack(cf.x, cf.y)), add);
                     }
                 }
                 if (!full) {
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r)
-                        x[r] = row0 + r >= r_min ? x[r] : -INFINITY;
+                    for (int r = 0; r < kRW; r += 2) {
+                        float x0, x1;
+                        f2_unpack(x[r / 2], x0, x1);
+                        x[r / 2] = f2_pack(row0 + r >= r_min ? x0 : -INFINITY,
+                                           row0 + r + 1 >= r_min ? x1 : -INFINITY);
+                    }
                 }
 #pragma unroll
-                for (int r = 0; r < kRW; r += 2)
-                    top = fmax3(top, x[r], x[r + 1]);
+                for (int r = 0; r < kRW; r += 2) {
+                    float x0, x1;
+                    f2_unpack(x[r / 2], x0, x1);
+                    top = fmax3(top, x0, x1);
+                }
                 return top;
             };
             if (t == 0 || bar_any(2 + wg, 128, exponents(false) > kQ8Unit + kQ8Grow)) {
@@ -917,10 +943,15 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 // the tile.
                 exponents(true);
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const int m = __reduce_max_sync(0xffffffffu, ordered(x[r]));
-                    if (lane == 0)
-                        s_red[warp][r] = m;
+                for (int r = 0; r < kRW; r += 2) {
+                    float x0, x1;
+                    f2_unpack(x[r / 2], x0, x1);
+                    const int m0 = __reduce_max_sync(0xffffffffu, ordered(x0));
+                    const int m1 = __reduce_max_sync(0xffffffffu, ordered(x1));
+                    if (lane == 0) {
+                        s_red[warp][r] = m0;
+                        s_red[warp][r + 1] = m1;
+                    }
                 }
                 bar_sync(2 + wg, 128);
                 if (tk < kRW) {
@@ -936,9 +967,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 bar_sync(2 + wg, 128);
                 if (t > 0) {
                     // P.V(t - 1) has to land before O is rescaled (tile 0 has no O yet).
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
-                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                    if (!warp_wait(b_o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1u, abort_flag))
                         ok = false;
                     tc_fence_after();
 #pragma unroll 1
@@ -958,8 +987,8 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                     tmem_st_wait();
                 }
 #pragma unroll
-                for (int r = 0; r < kRW; ++r)
-                    x[r] += s_nm[row0 + r];
+                for (int r = 0; r < kRW; r += 2)
+                    x[r / 2] = f2_add(x[r / 2], f2_pack(s_nm[row0 + r], s_nm[row0 + r + 1]));
 #pragma unroll
                 for (int r = 0; r < kRW; r += 2)
                     l2[r / 2] = f2_mul(l2[r / 2], f2_pack(s_al[row0 + r], s_al[row0 + r + 1]));
@@ -968,15 +997,8 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             // ---- weights, their sums, and their four parts -> this token's row of P,
             // once P.V(t - kBuf) has read the buffer
             if (t >= C::kBuf &&
-                !__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((t - C::kBuf) & 1),
-                                                             (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag)))
+                !warp_wait(b_o_done + 8 * ((t - C::kBuf) & 1), (uint32_t)((t - C::kBuf) >> 1) & 1u, abort_flag))
                 ok = false;
-            const uint32_t prow = p_sm + (uint32_t)j * C::kPBytes + tk * C::kPW;
-            // 16-byte chunk c of the row, as the swizzle places it.
-            auto chunk = [&](int c) -> uint32_t {
-                constexpr int kLg = C::kPW == 128 ? 0 : C::kPW == 64 ? 1 : 2;
-                return (uint32_t)(c ^ ((tk >> kLg) & (C::kPW / 16 - 1))) << 4;
-            };
             uint32_t w[4][kRW / 4]; // part k of rows 4 i .. 4 i + 3
             const uint64_t rl2 = f2_pack(rl, rl);
 #pragma unroll
@@ -984,7 +1006,9 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 uint32_t h[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float w0 = fast_exp2(x[r + 2 * q]), w1 = fast_exp2(x[r + 2 * q + 1]);
+                    float x0, x1;
+                    f2_unpack(x[r / 2 + q], x0, x1);
+                    const float w0 = fast_exp2(x0), w1 = fast_exp2(x1);
                     l2[r / 2 + q] = f2_fma(f2_pack(w0, w1), rl2, l2[r / 2 + q]);
                     h[q] = Elem<__half>::pack(w0, w1);
                 }
@@ -997,20 +1021,19 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                     }
                 }
             }
+            const uint32_t pj = prow + (uint32_t)j * C::kPBytes;
             if constexpr (kRW == 16) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int n = k * NR + row0;
-                    const uint32_t dst = prow + (n / C::kPW) * C::kPGroup + chunk(n % C::kPW / 16);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[k][0]),
-                                 "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     (pj ^ (k * NR % C::kPW)) + k * NR / C::kPW * C::kPGroup),
+                                 "r"(w[k][0]), "r"(w[k][1]), "r"(w[k][2]), "r"(w[k][3])
                                  : "memory");
-                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; k += 2)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(prow + chunk(k / 2)),
-                                 "r"(w[k][0]), "r"(w[k][1]), "r"(w[k + 1][0]), "r"(w[k + 1][1])
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(pj ^ (k * 8)), "r"(w[k][0]),
+                                 "r"(w[k][1]), "r"(w[k + 1][0]), "r"(w[k + 1][1])
                                  : "memory");
             }
             if (t == ntiles - 1) {
@@ -1023,12 +1046,9 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                     // landed, which P.V(t - kBuf), done by now, says for a ring of kBuf
                     // stages or more; a shorter one waits for P.V(t - 1) first.
                     if (vst < C::kBuf && t > 0 &&
-                        !__all_sync(0xffffffffu,
-                                    mbar_wait_abortable(b_o_done + 8 * ((t - 1) & 1),
-                                                        (uint32_t)((t - 1) >> 1) & 1u, abort_flag)))
+                        !warp_wait(b_o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1u, abort_flag))
                         ok = false;
-                    if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_v_full + 8 * s,
-                                                                     (uint32_t)(t / vst) & 1u, abort_flag)))
+                    if (!warp_wait(b_v_full + 8 * s, (uint32_t)(t / vst) & 1u, abort_flag))
                         ok = false;
                     const uint32_t vb = v_sm + (uint32_t)s * C::kTile;
                     constexpr int kChunks = C::kRB / 16;
@@ -1087,8 +1107,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         }
         bar_sync(2 + wg, 128);
         // P.V(ntiles - 1), the last MMA.
-        if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_o_done + 8 * ((ntiles - 1) & 1),
-                                                    (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag)))
+        if (!warp_wait(b_o_done + 8 * ((ntiles - 1) & 1), (uint32_t)((ntiles - 1) >> 1) & 1u, abort_flag))
             ok = false;
         tc_fence_after();
         if (!ok) {

@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(kCopyThreads) q8_copy_kernel(const Q8CopyParam
                     if (i >= pieces)
                         continue;
                     const int h = i >> lg_head;
-                    const float s = __ldg(scales + h);
+                    float s = __ldg(scales + h);
+                    if (which && !(s >= 0.f && s <= 3.4028234663852886e38f))
+                        s = NAN; // as in the 8-bit kernel
                     // Codes but for their signs.
                     const uint32_t any = (x[u].x | x[u].y | x[u].z | x[u].w) & 0x7f7f7f7fu;
                     const bool half_out = VH ? which == 1 : sizeof(T) == 2 && !Elem<T>::kSplitP;

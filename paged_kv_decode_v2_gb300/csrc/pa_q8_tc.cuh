@@ -281,7 +281,7 @@ __device__ __forceinline__ void join_cluster(uint32_t o_sm, uint32_t ml, int ran
         float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kQ8Ways; ++w) {
-            if (l[w] > 0.f) { // (an empty one's o may be anything)
+            if (!(l[w] == 0.f)) { // (an empty one's o may be anything)
                 const float f = l[w] * fast_exp2(m[w] - top);
                 sum += f;
                 x[0] += f * o[w].x;
@@ -290,7 +290,7 @@ __device__ __forceinline__ void join_cluster(uint32_t o_sm, uint32_t ml, int ran
                 x[3] += f * o[w].w;
             }
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint32_t *const dst = reinterpret_cast<uint32_t *>(out + row_of(r) * D + d);
         dst[0] = E::pack(x[0] * inv, x[1] * inv);
         dst[1] = E::pack(x[2] * inv, x[3] * inv);
@@ -317,6 +317,7 @@ struct Q8Cfg {
     static constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static constexpr uint32_t kSCol = kOReg * kMB;
     static_assert(kNeed <= 512, "O and S exceed the tensor memory");
+    static_assert(NR * D * 4 <= 2 * kTile, "a cluster's partials lie in the smallest rings");
     static constexpr int kPW = kPN <= 32 ? 32 : kPN <= 64 ? 64 : 128; // bytes of P's rows, and
     static constexpr int kPGroups = (kPN + kPW - 1) / kPW;        // groups of that many columns
     static constexpr uint32_t kPGroup = kQ8Tok * kPW;
@@ -813,9 +814,12 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         // The range's scales (the first S runs meanwhile): the largest V scale of
         // all, and the first chapter into shared memory.
-        vref = fmaxf(vref, vs_first);
-        for (int j = threadIdx.x + C::kSoft; j < nblk; j += C::kSoft)
-            vref = fmaxf(vref, __ldg(p.v_scales + (size_t)valid_id(__ldg(bt + j)) * p.num_kv_heads + kv));
+        auto usable = [](float v) { return v >= 0.f && v <= 3.4028234663852886e38f; };
+        vref = fmaxf(vref, usable(vs_first) ? vs_first : 0.f);
+        for (int j = threadIdx.x + C::kSoft; j < nblk; j += C::kSoft) {
+            const float v = __ldg(p.v_scales + (size_t)valid_id(__ldg(bt + j)) * p.num_kv_heads + kv);
+            vref = fmaxf(vref, usable(v) ? v : 0.f);
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
@@ -827,11 +831,13 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             vref = fmaxf(vref, s_vref[w]);
         const float vref_lg = fast_log2(vref);
         // Blocks that are not there get ks = 0 and any lv.
+        // A V scale that is negative or not finite: weights of NaN for who sees the block.
         auto put_scales = [&](int i, float k, float v) {
-            const float lv = fmaxf(fast_log2(v) - vref_lg, kQ8Floor);
+            const bool good = usable(v);
+            const float lv = good ? fmaxf(fast_log2(v) - vref_lg, kQ8Floor) : NAN;
             s_ks[i] = k;
             s_lv[i] = lv;
-            s_rl[i] = fast_exp2(-lv);
+            s_rl[i] = good ? fast_exp2(-lv) : 1.f;
         };
         auto load_chapter = [&](int j0, int i0) { // blocks j0 + i, i >= i0
             for (int i = i0 + threadIdx.x; i < C::kChap; i += C::kSoft) {
@@ -1096,7 +1102,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             for (int w = 1; w < 4; ++w)
                 sum += s_part[wg * 4 + w][tk];
             const int r = row0 + tk;
-            s_inv[r] = sum > 0.f ? vref / sum : 0.f; // O and l hold weights in the same unit
+            s_inv[r] = sum == 0.f ? 0.f : vref / sum; // O and l hold weights in the same unit
             if (V1) {
                 s_ml[r] = sum > 0.f ? kQ8Unit - s_nm[r] : -INFINITY;
                 s_ml[NR + r] = sum;

@@ -207,6 +207,63 @@ def test_hint_and_long_cache(pa):
 
 
 @gpu
+@pytest.mark.parametrize("what", ["k code", "v code", "k scale", "v scale", "v scale < 0", "v scale inf"])
+@pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([300, 90], 64, 2), ([1100, 40], 2048, 1), ([6000, 90], 64, 3),
+                                      ([500] * 160, 512, 1), ([120, 700], 2048, 70)])
+def test_nan_is_not_lost(pa, lens, P, Q, what):
+    """V1 on one CTA and on a cluster, V2, sorted units, the 16-bit copy: NaN reaches what sees it, and nothing else."""
+    kc, vc, ks, vs, tables, lens = c = cu.cache8(lens, KV=2, D=64, bs=16)
+    block = int(tables[0, 2]) # tokens 32 to 47
+    target = {"k code": kc, "v code": vc, "k scale": ks}.get(what, vs)
+    if "code" in what:
+        target.view(torch.uint8)[block, 1, 3, 5] = 0x7f
+    else:
+        target[block, 1] = {"v scale < 0": -1.0, "v scale inf": math.inf}.get(what, math.nan)
+    q = torch.randn((len(lens), Q, 8, 64)).to(BF16)
+    out, status = run(pa, q, c, 0.125, P)
+    assert status == 0
+    bad = torch.isnan(out)
+    seen = torch.tensor([int(lens[0]) - Q + i >= 47 for i in range(Q)])
+    if what == "v code":  # the one dim; and of new tokens that do not see it as well (0 * NaN)
+        assert bad[0, seen][:, 4:, 5].all()
+        bad[0, :, 4:, 5] = False
+    else:
+        assert bad[0, seen][:, 4:].all()
+        bad[0, :, 4:] &= ~torch.tensor([int(lens[0]) - Q + i >= 32 for i in range(Q)])[:, None, None]
+    assert not bad.any()
+
+
+@gpu
+@pytest.mark.parametrize("dtype,G,Q", [(BF16, 2, 1), (F16, 12, 1), (BF16, 2, 30)])
+@pytest.mark.parametrize("S", [150, 256, 257])
+def test_many_sequences(pa, S, dtype, G, Q):
+    """More units than the GPU holds: sorted by size up to 256 sequences; V1 (short ones) and V2."""
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(0, 70, (S,), generator=g)
+    lens[::17] = 0
+    lens[5:140:45] = torch.tensor([300, 128, 511])
+    check(pa, lens.tolist(), KV=2, G=G, Q=Q, D=64, bs=16, P=512, dtype=dtype)
+    lens[7:140:45] = torch.tensor([9000, 8192, 4100])  # (partitions: where a sequence has more than 8192 tokens)
+    assert pa.pa_decode_q8_partition(S, Q, 2 * G, 2, 64, 9040, 64) > 0
+    check(pa, lens.tolist(), KV=2, G=G, Q=Q, D=64, bs=16, P=64, dtype=dtype)
+
+
+@gpu
+def test_status_of_many_sequences(pa):
+    c = list(cu.cache8([33] * 200, bs=16))
+    c[4].clamp_(min=0)
+    q = torch.randn((200, 1, 8, 64)).to(F16)
+    clean, status = run(pa, q, c, 0.125, 512)
+    assert status == 0
+    for bad in (-1, 10 ** 6):
+        c[5][150] = bad
+        out, status = run(pa, q, c, 0.125, 512)
+        assert status == pa.PA_STATUS_BAD_SEQ_LEN
+        rest = [b for b in range(200) if b != 150]
+        assert torch.equal(out[rest], clean[rest]) and (bad > 0 or (out[150] == 0).all())
+
+
+@gpu
 @pytest.mark.parametrize("Q", [1, 20])
 def test_status(pa, Q):
     c = list(cu.cache8([40, 100], bs=16))

@@ -477,10 +477,19 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     const int bpt = kQ8Tok >> sh;               // blocks per tile: 2 to 16
     const int blk0 = tokA >> sh;
     const int32_t *bt = p.block_tables + (size_t)b * p.max_blocks + blk0;
-    // The table's first entries, loaded beside the length.
+    // A producer warp loads all or half the blocks of every K or V tile: one warp
+    // issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80 clocks each)
+    // would bound the loop of few rows.
+    constexpr int kSplit = C::kLoad / 2; // producer warps of one tile
+    const int pw = warp - kTmaWarp;
+    const bool is_k = pw < kSplit;
+    const int p_num = bpt / kSplit, p_first = pw % kSplit * p_num; // its blocks of a tile
+    // The table's first entries, loaded beside the length: block threadIdx.x of a
+    // softmax thread, a producer lane's block of the first tile.
     int32_t id_first = 0;
-    if (threadIdx.x < C::kSoft && blk0 + (int)threadIdx.x < p.max_blocks)
-        id_first = __ldg(bt + threadIdx.x);
+    const int at_first = warp < kTmaWarp ? (int)threadIdx.x : p_first + lane;
+    if ((warp < kMmaWarp || (warp >= kTmaWarp && lane < p_num)) && blk0 + at_first < p.max_blocks)
+        id_first = __ldg(bt + at_first);
     if (!p.sorted)
         L = length(b, reporter && part == 0 && threadIdx.x == 0);
     if (!V1 && tokA >= L)
@@ -554,13 +563,6 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         tmem_relinquish();
     }
     int32_t status_bits = 0;
-    // A producer warp loads all or half the blocks of every K or V tile: one warp
-    // issuing all of a tile's TMA loads (16 at 16-token blocks, 40-80 clocks each)
-    // would bound the loop of few rows.
-    constexpr int kSplit = C::kLoad / 2; // producer warps of one tile
-    const int pw = warp - kTmaWarp;
-    const bool is_k = pw < kSplit;
-    const int p_num = bpt / kSplit, p_first = pw % kSplit * p_num; // its blocks of a tile
     const int p_stages = is_k ? kst : vst;
     const uint32_t p_full_bar = is_k ? b_k_full : b_v_full, p_empty_bar = is_k ? b_k_empty : b_v_empty;
     const uint32_t p_ring = is_k ? k_sm : v_sm;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     if (warp >= kTmaWarp) {
         // The first tiles, before the rest of the set-up.
         bar_sync(15, 32 * C::kLoad); // the barriers are initialised
-        id_next = fetch_id(0);
+        id_next = lane < p_num && p_first + lane < nblk ? id_first : 0;
         while (issued < ntiles && issued < p_stages) {
             const int32_t id = id_next;
             id_next = fetch_id(issued + 1);

@@ -564,7 +564,7 @@ int v2_phase1_impl(const void *query, const void *key_cache, const void *value_c
 int v2_phase2_impl(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
                    int max_seq_len, int partition_size, int dtype, const float *tmp_output,
                    const float *exp_sums, const float *max_logits, int max_num_partitions,
-                   void *out, int32_t *status, cudaStream_t stream)
+                   void *out, int32_t *status, cudaStream_t stream, bool single_done = false)
 {
     if (!seq_lens || !tmp_output || !exp_sums || !max_logits || !out)
         return PA_ERR_INVALID_ARG;
@@ -598,6 +598,7 @@ int v2_phase2_impl(const int32_t *seq_lens, int num_seqs, int q_len, int num_hea
     p.max_logits = max_logits;
     p.out = out;
     p.status = status;
+    p.single_done = single_done;
     int dev;
     if (current_device(&dev))
         return PA_ERR_CUDA;
@@ -948,11 +949,11 @@ int host_mq_over_copy(const void *query, const void *k, const void *v, bool v_ha
 int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
                int max_seq_len, int partition_size, int dtype, const float *tmp_output,
                const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
-               int32_t *status, cudaStream_t stream)
+               bool single_done, int32_t *status, cudaStream_t stream)
 {
     return v2_phase2_impl(seq_lens, num_seqs, q_len, num_heads, head_dim, max_seq_len,
                           partition_size, dtype, tmp_output, exp_sums, max_logits,
-                          max_num_partitions, out, status, stream);
+                          max_num_partitions, out, status, stream, single_done);
 }
 
 } // namespace pa

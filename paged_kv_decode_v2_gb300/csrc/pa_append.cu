@@ -9,6 +9,11 @@
 // dims pass unchanged.  It is computed in fp32 and rounded once, to the
 // storage type (or straight to 8 bits).
 //
+// Measured on a GB300 (us a call, share of the measured copy bandwidth): 64 prompts
+// of up to 2048 tokens, 64 heads on 8, 128 dims: 410 (98%), to 8 bits 404 (94%);
+// two chunks of 2048 tokens, 32 heads on 8, to 8 bits: 18.5 (75%); 32 single tokens
+// to 8 bits 3.2, one token 2.6 (latency and launch).
+//
 // 16-bit caches: a pure copy with three operations per value, bound by bytes
 // on prompts and by its chain of dependent loads (starts -> length -> block
 // id -> store) on single tokens.  One CTA per token: a thread keeps one pair
@@ -24,7 +29,8 @@
 // fall into e4m3's subnormals), so rounding does not build up as a block is
 // filled token by token.  One CTA owns one (block, KV head) -- its rows times
 // pairs of chunks are its threads -- so the maximum is a reduction inside the
-// CTA and no two CTAs write one scale.
+// CTA and no two CTAs write one scale.  Splitting K and V over CTAs, and four
+// rows per thread in flight, were slower.
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -37,8 +43,9 @@ namespace pa {
 namespace {
 
 constexpr int kAppendThreads = 128;
-constexpr int kAppendRounds = 2; // rows per thread in flight
-constexpr int kAppendCtas = 8;   // per SM
+// Rows per thread in flight and CTAs per SM: prompts 410 us, 420 with four rows.
+constexpr int kAppendRounds = 2;
+constexpr int kAppendCtas = 8;
 
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
@@ -655,8 +662,10 @@ long long append_q8_ctas(const AppendParams &p)
     return append_q8_items(p) * p.num_kv_heads + (p.num_heads ? p.num_tokens : 0);
 }
 
-constexpr int kMaxHeads = 8;     // KV heads of a CTA at most
-constexpr int kApartTokens = 60; // tokens per SM from which queries get their own launch
+constexpr int kMaxHeads = 8; // KV heads of a CTA at most
+// Tokens per SM from which queries get their own launch: prompts (some 430 per SM) 404
+// us, 445 in one launch; two chunks (27 per SM) 24.4 us, 18.7 in one launch.
+constexpr int kApartTokens = 60;
 
 static int log2_of(int x) // of a power of two
 {

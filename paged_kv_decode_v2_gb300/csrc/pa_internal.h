@@ -87,6 +87,7 @@ struct MergeParams {
     const float *max_logits;
     void *out;
     int32_t *status;
+    bool single_done;            // phase 1 wrote the outputs of sequences of one partition
 };
 
 // The binary16 copy of the V blocks a multi-query call reads (bf16 caches):

@@ -73,6 +73,10 @@ __global__ void __launch_bounds__(NTH) merge_kernel(const MergeParams p)
             out[threadIdx.x] = E::from_float(0.f);
         return;
     }
+    if (p.single_done && np == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory"); // this grid ends after phase 1
+        return;
+    }
     const float *ml = p.max_logits + bh * p.max_num_partitions;
     const float *es = p.exp_sums + bh * p.max_num_partitions;
     const float4 *tmp = reinterpret_cast<const float4 *>(p.tmp_output + bh * p.max_num_partitions * D + d0);
@@ -164,6 +168,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergePa
 #pragma unroll
         for (int j = 0; j < DL; ++j)
             out[j] = E::from_float(0.f);
+        return;
+    }
+    if (p.single_done && np == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     const float *ml = p.max_logits + (size_t)pair * p.max_num_partitions;

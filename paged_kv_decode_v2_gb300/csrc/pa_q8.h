@@ -24,7 +24,7 @@ void host_tuning(int *warps, int *stages, int *rows_kernel);
 int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,
                int max_seq_len, int partition_size, int dtype, const float *tmp_output,
                const float *exp_sums, const float *max_logits, int max_num_partitions, void *out,
-               int32_t *status, cudaStream_t stream);
+               bool single_done, int32_t *status, cudaStream_t stream);
 
 // The 16-bit multi-query attention over copies of K and V (partials at a stride
 // of np partitions of `part` tokens, V1 when part is 0), bf16 with V's binary16

@@ -255,8 +255,8 @@ struct Q8Cut {
 // kWavePart tokens each: one sequence of 100,000 tokens, 4 KV heads: 1408 tokens 21.4
 // us, 2048 22.7, 1024 27.2.  Else two waves or more, sorted by size (see the kernel),
 // the fewest whose partitions have at most kMaxPart tokens: 32 sequences of up to 8192,
-// 8 KV heads: 4096 53 us, 2048 55, 8192 60; 64 of up to 32,768: 8192 76 us, 4096 85,
-// 16,384 112; 16 new tokens for 32 of up to 8192: 8192 93 us, 4096 104.
+// 8 KV heads: 4096 52 us, 2048 54, 8192 59; 64 of up to 32,768: 8192 74 us, 4096 84,
+// 16,384 112; 16 new tokens for 32 of up to 8192: 8192 89 us, 4096 98.
 constexpr int kWavePart = 2048, kMaxPart = 8192;
 // V1 unless a CTA of its cluster has more tiles than a partition by more than this:
 // what the second launch costs (8 groups of 8000 tokens: V2 10.5 us at 4 tiles, V1
@@ -298,7 +298,9 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
 // ---- the 16-bit copy for many rows
 
 // From this many query rows per KV head on, the call makes a 16-bit copy of its
-// blocks and runs the 16-bit kernels over it.
+// blocks and runs the 16-bit kernels over it.  8 KV heads, copy / 8-bit kernel, us: 2
+// sequences of 9000 tokens 128 rows 56 / 52, 256 rows 67 / 82, 1024 rows 116 / 259;
+// 16 of 2000 86 / 75, 99 / 146, 247 / 489.
 constexpr int kQ8CopyRows = 256;
 
 struct CopyPlan {
@@ -536,7 +538,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     if (rc || L.v1)
         return rc;
     return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
-                      exp_sums, max_logits, max_num_partitions, out, status, st);
+                      exp_sums, max_logits, max_num_partitions, out, true, status, st);
 }
 
 } // extern "C"

@@ -43,9 +43,25 @@
 //
 // Warp roles: warpgroups of softmax warps (16 rows each at most; thread = token
 // = TMEM lane, and dim in the epilogue), one warp that issues the MMAs of S (and
-// owns the tensor memory), one that issues those of P.V, two or four that issue the TMA loads.
-// S and P have two buffers where tensor memory allows (else one): S of tile
-// t + 2 is issued once the softmax has read S of tile t.
+// owns the tensor memory), one that issues those of P.V, two or four that issue
+// the TMA loads.  S and P have two buffers where tensor memory allows (else one):
+// S of tile t + 2 is issued once the softmax has read S of tile t.
+//
+// Rows beyond NR go to more CTAs, tokens are cut into partitions (V2) or over a
+// cluster (V1, joined through distributed shared memory).  Where CTAs queue they
+// take units of work in order of size.
+//
+// Measured on a GB300 (us a call, and its bytes as a share of the measured copy
+// bandwidth): 32 sequences of up to 8192 tokens, 32 heads on 8: 52 (80%); one of
+// 100,000 tokens on 4 KV heads: 21.7 (70%); 64 of up to 32,768, 64 heads on 8: 73
+// (82%); 8 of 131,072: 323 (98%); one of 1000: 7.0, latency.  16 new tokens for 32
+// sequences: 89 (46%), bound by the softmax warps: some 400 instructions a warp and
+// tile, about 140 of them arithmetic, more than half of that the parts of P and Q.
+//
+// Built and measured slower: the same work on mma.sync (16 new tokens 278); equal
+// stretches of tiles over a fixed grid (16 new tokens 166 where partitions took
+// 121, ragged 96 and 89); 32 rows a softmax warpgroup (100 and 92); two CTAs of 32
+// rows for 64 (107 and 92); waits that spin, or suspend at the first try (96 and 92).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -415,8 +431,8 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         const int at = threadIdx.x;
         const int len = at < p.num_seqs ? length(at, reporter && unit == 0) : 0;
         const int size = V1 ? p.seq_len_cap : p.partition_size;
-        const int whole = V1 ? 0 : len / size;
-        const int rest = len - whole * size;
+        const int parts = V1 ? 0 : len / size; // whole ones
+        const int rest = len - parts * size;
         int cls = -1; // 0 (largest) to 31; none without a unit
         if (V1 ? at < p.num_seqs : rest > 0)
             cls = min((int)((float)(size - rest) * p.class_scale), 31);
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         const int ahead = __popc(peers & ((1u << lane) - 1u));
         if (cls >= 0 && ahead == 0)
             s_count[warp][cls] = __popc(peers);
-        int run = whole; // inclusive scan
+        int run = parts; // inclusive scan
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, run, off);
@@ -438,7 +454,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             s_whole[warp] = run;
         __syncthreads();
         const int used = (p.num_seqs + 31) / 32; // warps that hold sequences
-        int total = 0, start = run - whole, count = 0, before = 0;
+        int total = 0, start = run - parts, count = 0, before = 0;
         for (int w = 0; w < used; ++w) {
             const int n = s_whole[w], c = s_count[w][lane];
             total += n;
@@ -453,10 +469,10 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             up += lane >= off ? v : 0;
         }
         const int first = __shfl_sync(0xffffffffu, total + up - count + before, cls & 31) + ahead;
-        const bool in_whole = unit >= start && unit - start < whole;
+        const bool in_whole = unit >= start && unit - start < parts;
         if (in_whole || (cls >= 0 && unit == first)) {
             s_pick[0] = at;
-            s_pick[1] = in_whole ? unit - start : whole;
+            s_pick[1] = in_whole ? unit - start : parts;
             s_pick[2] = len;
         }
         __syncthreads();
@@ -494,6 +510,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         L = length(b, reporter && part == 0 && threadIdx.x == 0);
     if (!V1 && tokA >= L)
         return; // partition past the end of the sequence: nothing to write
+    const bool whole = V1 || L <= p.partition_size; // the output itself, no partials
 
     // Rows [c0, c0 + nrows) of the KV head's cols = q_len * group rows.
     const int c0 = rt * NR;
@@ -520,7 +537,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     const uint32_t smem0 = (smem_addr(dyn_smem) + 1023u) & ~1023u;
     if (ntiles == 0) {
         // No row sees a token of the range: an empty partition (m = -inf,
-        // l = 0, o = 0), or a zero output in V1.
+        // l = 0, o = 0), or a zero output.
         if (V1 && ways > 1) {
             if (threadIdx.x < NR) {
                 s_ml[threadIdx.x] = -INFINITY;
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         }
         for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
             const size_t row = row_of(idx / D);
-            if (V1) {
+            if (whole) {
                 static_cast<T *>(p.out)[row * D + idx % D] = E::from_float(0.f);
             } else {
                 const size_t slot = row * p.max_num_partitions + part;
@@ -668,7 +685,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 s_cf[r] = p.scale * inv * kLog2e;
                 s_nm[r] = -kQ8NoMax;
                 const size_t row = row_of(r < nrows ? r : 0);
-                s_row[r] = V1 ? row : row * p.max_num_partitions + part;
+                s_row[r] = whole ? row : row * p.max_num_partitions + part;
             }
 #pragma unroll
             for (int k = 0; k < kDL; ++k) // a value that is not finite becomes NaN
@@ -1108,7 +1125,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             if (V1) {
                 s_ml[r] = sum > 0.f ? kQ8Unit - s_nm[r] : -INFINITY;
                 s_ml[NR + r] = sum;
-            } else if (r < nrows) {
+            } else if (!whole && r < nrows) {
                 p.exp_sums[s_row[r]] = sum * 4.8828125e-4f; // 2^-11
                 p.max_logits[s_row[r]] = sum > 0.f ? (kQ8Unit - s_nm[r]) * kQ8Ln2 : -INFINITY;
             }
@@ -1147,7 +1164,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                             if (V1 && ways > 1) // every tile of the rings is read by now
                                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem0 + (r * D + d) * 4), "f"(v)
                                              : "memory");
-                            else if (V1)
+                            else if (whole)
                                 static_cast<T *>(p.out)[s_row[r] * D + d] = E::from_float(v);
                             else
                                 p.tmp_output[s_row[r] * D + d] = v;

@@ -115,7 +115,8 @@ struct Q8Params {
     float *exp_sums;
     float *max_logits;
     void *out;                   // V1
-    const int32_t *only_if;      // run only if this word is not 0 (null: always)
+    const int32_t *only_if;      // kQ8If: run only if this word is not 0,
+    int units;                   // a CTA's share of so many
     int32_t *status;
 };
 
@@ -143,7 +144,7 @@ struct Q8Launch {
     CUtensorMap tmap_v;
     int head_dim;
     int block_size;
-    bool v1;
+    int mode;                    // kQ8V2, ..
     dim3 grid;
     size_t smem_bytes;
 };
@@ -152,6 +153,7 @@ struct Q8Launch {
 constexpr int kQ8Tok = 128; // tokens per tile
 constexpr int kQ8Sorted = 256; // sequences that a CTA's threads sort
 constexpr int kQ8Ways = 8;  // CTAs of a cluster at most (the portable size)
+enum { kQ8V2, kQ8V1, kQ8If }; // kQ8If: V1 if a flag is up, any grid
 struct Q8TcKernel {
     const void *fn;
     int threads;
@@ -159,15 +161,15 @@ struct Q8TcKernel {
     size_t fixed_bytes;      // dynamic shared memory but for the rings
 };
 // rows 8, 16, 32, or (up to head_dim 128) 64; fn null otherwise.
-Q8TcKernel q8_tc_d64(int rows, int dtype, bool v1);
-Q8TcKernel q8_tc_d128(int rows, int dtype, bool v1);
-Q8TcKernel q8_tc_d256(int rows, int dtype, bool v1);
+Q8TcKernel q8_tc_d64(int rows, int dtype, int mode);
+Q8TcKernel q8_tc_d128(int rows, int dtype, int mode);
+Q8TcKernel q8_tc_d256(int rows, int dtype, int mode);
 
-inline Q8TcKernel q8_tc(int head_dim, int rows, int dtype, bool v1)
+inline Q8TcKernel q8_tc(int head_dim, int rows, int dtype, int mode)
 {
-    return head_dim == 64    ? q8_tc_d64(rows, dtype, v1)
-           : head_dim == 128 ? q8_tc_d128(rows, dtype, v1)
-                             : q8_tc_d256(rows, dtype, v1);
+    return head_dim == 64    ? q8_tc_d64(rows, dtype, mode)
+           : head_dim == 128 ? q8_tc_d128(rows, dtype, mode)
+                             : q8_tc_d256(rows, dtype, mode);
 }
 
 } // namespace pa

@@ -29,17 +29,17 @@ int rows_per_cta(int cols, int head_dim)
 // CTAs of the kernel that share an SM.
 int ctas_per_sm(int nr, int head_dim) { return nr <= 32 && head_dim <= 128 ? 2 : 1; }
 
-std::atomic<int64_t> g_tc_limit[kMaxDevices][3 * 4 * 2 * 2];
+std::atomic<int64_t> g_tc_limit[kMaxDevices][3 * 4 * 2 * 3];
 
 int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
 {
-    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype, L.v1);
+    const Q8TcKernel k = q8_tc(L.head_dim, nr, L.p.dtype, L.mode);
     if (!k.fn)
         return PA_ERR_UNSUPPORTED;
     const int di = L.head_dim == 64 ? 0 : L.head_dim == 128 ? 1 : 2;
     const int ri = nr == 8 ? 0 : nr == 16 ? 1 : nr == 32 ? 2 : 3;
     std::atomic<int64_t> &cell =
-        g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 2 + (L.v1 ? 1 : 0)];
+        g_tc_limit[dev][((di * 4 + ri) * 2 + (L.p.dtype == PA_BF16 ? 1 : 0)) * 3 + L.mode];
     // Dynamic limit after the opt-in in the low half, static bytes above.
     int64_t have = cell.load(std::memory_order_acquire);
     if (have == 0) {
@@ -103,7 +103,7 @@ int launch_tc(Q8Launch &L, int dev, int nr, cudaStream_t stream)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = L.v1 && L.p.ways > 1 ? 2 : 1;
+    cfg.numAttrs = L.mode == kQ8V1 && L.p.ways > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, k.fn, args) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -501,7 +501,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     p.status = status;
     L.head_dim = head_dim;
     L.block_size = block_size;
-    L.v1 = part == 0;
+    L.mode = part == 0 ? kQ8V1 : kQ8V2;
 
     if (work_ok && p.cols >= kQ8CopyRows) {
         Q8CopyParams c = {};
@@ -520,22 +520,23 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
             // Values that binary16 cannot hold: the 8-bit kernel runs after all (V1,
             // which needs no intermediates, over the result above).
             p.only_if = c.flag;
-            L.v1 = true;
+            L.mode = kQ8If;
             p.ways = 1;
         }
     }
-    const long long gx = (long long)num_seqs * num_kv_heads * p.col_groups * (L.v1 ? p.ways : np);
+    const long long gx = (long long)num_seqs * num_kv_heads * p.col_groups * (L.mode == kQ8V2 ? np : p.ways);
     if (gx > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    L.grid = dim3((unsigned)gx);
+    p.units = (int)gx;
+    L.grid = dim3((unsigned)(L.mode == kQ8If ? std::min(gx, (long long)sms) : gx));
     // By size where CTAs wait for their turn (the sort costs each some 0.4 us).
     p.num_seqs = num_seqs;
     p.num_parts = np;
-    p.class_scale = 32.f / (float)(L.v1 ? cap : part);
-    p.sorted = num_seqs > 1 && num_seqs <= kQ8Sorted && p.ways == 1 &&
+    p.class_scale = 32.f / (float)(L.mode == kQ8V2 ? part : cap);
+    p.sorted = L.mode != kQ8If && num_seqs > 1 && num_seqs <= kQ8Sorted && p.ways == 1 &&
                gx > (long long)sms * ctas_per_sm(rows_per_cta(p.cols, head_dim), head_dim);
     rc = launch_tc(L, dev, rows_per_cta(p.cols, head_dim), st);
-    if (rc || L.v1)
+    if (rc || L.mode != kQ8V2)
         return rc;
     return host_merge(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, part, dtype, tmp_output,
                       exp_sums, max_logits, max_num_partitions, out, true, status, st);

@@ -185,6 +185,11 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8])
                    "+r"(r[6]), "+r"(r[7])::"memory");
 }
 
+__device__ __forceinline__ void mbar_inval(uint32_t bar)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -353,12 +358,11 @@ struct Q8Cfg {
     static constexpr uint32_t kFixed = 1024 + kBuf * kPBytes + kQBytes;
 };
 
-// (Registers are handed out to warps by fours: launch bounds of a multiple of 128
-// threads let two CTAs share an SM.)
-template <int D, int NR, int PL, bool V1>
-__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
-    q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                 const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
+// The work of CTA `bid` of the grid that p describes; false after a wait that gave up.
+// LOOP: one of several that a CTA takes, its barriers gone at the end.
+template <int D, int NR, int PL, bool V1, bool LOOP>
+__device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                        const Q8Params &p, int bid)
 {
     using C = Q8Cfg<D, NR, PL>;
     using T = typename std::conditional<PL == 2, __nv_bfloat16, __half>::type;
@@ -385,24 +389,14 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        prefetch_tensormap(&tmap_k);
-        prefetch_tensormap(&tmap_v);
-    }
-    // Programmatic stream serialisation: nothing global is touched before
-    // the previous grid in the stream has completed.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    if (p.only_if && __ldcg(p.only_if) == 0)
-        return;
 
-    // blockIdx.x = ((unit * KV + KV head) * row tiles + row tile) * ways + rank: units are
+    // bid = ((unit * KV + KV head) * row tiles + row tile) * ways + rank: units are
     // partitions of sequences (V1: sequences, the `ways` CTAs of a cluster their
     // partitions); row tiles of one KV head are neighbours, so that their reads meet
     // in L2.
     const int ways = V1 ? p.ways : 1;
-    int unit = V1 ? (int)blockIdx.x / ways : (int)blockIdx.x;
-    int part = V1 ? (int)blockIdx.x % ways : 0;
+    int unit = V1 ? bid / ways : bid;
+    int part = V1 ? bid % ways : 0;
     int rt = 0;
     if (p.col_groups > 1) {
         rt = unit % p.col_groups;
@@ -478,7 +472,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
         __syncthreads();
         b = s_pick[0];
         if (b < 0)
-            return; // past the last unit
+            return true; // past the last unit
         part = s_pick[1];
         L = s_pick[2];
     } else if (V1) {
@@ -509,7 +503,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     if (!p.sorted)
         L = length(b, reporter && part == 0 && threadIdx.x == 0);
     if (!V1 && tokA >= L)
-        return; // partition past the end of the sequence: nothing to write
+        return true; // partition past the end of the sequence: nothing to write
     const bool whole = V1 || L <= p.partition_size; // the output itself, no partials
 
     // Rows [c0, c0 + nrows) of the KV head's cols = q_len * group rows.
@@ -545,7 +539,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
             }
             __syncthreads();
             join_cluster<D, NR>(smem0, smem_addr(s_ml), part, ways, nrows, static_cast<T *>(p.out), row_of);
-            return;
+            return true;
         }
         for (int idx = threadIdx.x; idx < nrows * D; idx += C::kThreads) {
             const size_t row = row_of(idx / D);
@@ -560,7 +554,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
                 }
             }
         }
-        return;
+        return true;
     }
 
     const int kst = p.stages;   // K ring stages
@@ -577,7 +571,8 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
 
     if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(&tmem_base_sh), C::kCols);
-        tmem_relinquish();
+        if (!LOOP)
+            tmem_relinquish();
     }
     int32_t status_bits = 0;
     const int p_stages = is_k ? kst : vst;
@@ -1185,23 +1180,86 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
     }
     if (V1 && ways > 1)
         join_cluster<D, NR>(smem0, smem_addr(s_ml), part, ways, nrows, static_cast<T *>(p.out), row_of);
+    if (LOOP && threadIdx.x == 0) {
+        for (int s = 0; s < kst; ++s) {
+            mbar_inval(b_k_full + 8 * s);
+            mbar_inval(b_k_empty + 8 * s);
+        }
+        for (int s = 0; s < vst; ++s) {
+            mbar_inval(b_v_full + 8 * s);
+            mbar_inval(b_v_empty + 8 * s);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_inval(b_s_full + 8 * j);
+            mbar_inval(b_p_full + 8 * j);
+            mbar_inval(b_o_done + 8 * j);
+            mbar_inval(b_drained + 8 * j);
+        }
+    }
+    return !LOOP || abort_sh == 0;
 }
 
-// Kernel and shared memory of one head_dim for NR = 8, 16, 32 or 64 rows (64
-// up to head_dim 128).
-template <int D, int NR>
-static Q8TcKernel q8_tc_pick(int dtype, bool v1)
+// Before anything global is touched the previous grid in the stream has completed
+// (programmatic stream serialisation).
+__device__ __forceinline__ void q8_begin(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v)
 {
-    if (dtype == PA_BF16) {
-        using C = Q8Cfg<D, NR, 2>;
-        return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, true>)
-                   : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 2, false>),
-                C::kThreads, C::kCtas, C::kFixed};
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
     }
-    using C = Q8Cfg<D, NR, 3>;
-    return {v1 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, true>)
-               : reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, 3, false>),
-            C::kThreads, C::kCtas, C::kFixed};
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// (Registers are handed out to warps by fours: launch bounds of a multiple of 128
+// threads let two CTAs share an SM.)
+template <int D, int NR, int PL, bool V1>
+__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
+    q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
+{
+    q8_begin(tmap_k, tmap_v);
+    q8_unit<D, NR, PL, V1, false>(tmap_k, tmap_v, p, blockIdx.x);
+}
+
+// V1 after the 16-bit copy's attention: runs only if the copy's flag is up, mostly not,
+// so a CTA per SM takes all the work (two chunks of 1024 new tokens: 308 us, 314 with a
+// CTA for each unit, the wide CTAs leaving wave by wave; 31 of 390 on 3 heads 263, 282).
+template <int D, int NR, int PL>
+__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
+    q8_tc_if_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
+{
+    q8_begin(tmap_k, tmap_v);
+    if (__ldcg(p.only_if) == 0)
+        return;
+    for (int bid = blockIdx.x; bid < p.units; bid += gridDim.x) {
+        if (!q8_unit<D, NR, PL, true, true>(tmap_k, tmap_v, p, bid))
+            break;
+        fence_proxy_async(); // the next unit's tiles land where this one's lay
+        __syncthreads();
+    }
+}
+
+// Kernel and shared memory of one head_dim for NR = 8, 16, 32 or 64 rows (64 up to head_dim
+// 128); the conditional one for the widest NR, which calls of many rows use.
+template <int D, int NR, int PL>
+static Q8TcKernel q8_tc_pick_parts(int mode)
+{
+    using C = Q8Cfg<D, NR, PL>;
+    const void *fn = mode == kQ8V1   ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, PL, true>)
+                     : mode == kQ8V2 ? reinterpret_cast<const void *>(&q8_tc_kernel<D, NR, PL, false>)
+                                     : nullptr;
+    if constexpr (NR == (D == 256 ? 32 : 64)) {
+        if (mode == kQ8If)
+            fn = reinterpret_cast<const void *>(&q8_tc_if_kernel<D, NR, PL>);
+    }
+    return {fn, C::kThreads, C::kCtas, C::kFixed};
+}
+template <int D, int NR>
+static Q8TcKernel q8_tc_pick(int dtype, int mode)
+{
+    return dtype == PA_BF16 ? q8_tc_pick_parts<D, NR, 2>(mode) : q8_tc_pick_parts<D, NR, 3>(mode);
 }
 
 } // namespace pa

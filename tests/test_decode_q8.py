@@ -183,6 +183,13 @@ def test_many_rows(pa, D, bs, KV, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("D,bs,dtype", [(64, 16, F16), (64, 8, BF16), (128, 32, BF16), (128, 16, F16), (256, 64, F16)])
+def test_many_rows_that_no_copy_can_hold(pa, D, bs, dtype):
+    """More units of the 8-bit kernel than the GPU has SMs, after the copy's attention."""
+    check(pa, [320, 0, 301, 40], Q=300, G=4, KV=3, D=D, bs=bs, dtype=dtype, P=128, scales="wild")
+
+
+@gpu
 @pytest.mark.parametrize("Q", [1, 12])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 2.0])
 def test_softmax_scales(pa, scale, Q):

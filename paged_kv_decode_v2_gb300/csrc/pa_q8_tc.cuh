@@ -54,7 +54,7 @@
 // Measured on a GB300 (us a call, and its bytes as a share of the measured copy
 // bandwidth): 32 sequences of up to 8192 tokens, 32 heads on 8: 52 (80%); one of
 // 100,000 tokens on 4 KV heads: 21.7 (70%); 64 of up to 32,768, 64 heads on 8: 73
-// (82%); 8 of 131,072: 323 (98%); one of 1000: 7.0, latency.  16 new tokens for 32
+// (100%); 8 of 131,072: 323 (98%); one of 1000: 7.0, latency.  16 new tokens for 32
 // sequences: 89 (46%), bound by the softmax warps: some 400 instructions a warp and
 // tile, about 140 of them arithmetic, more than half of that the parts of P and Q.
 //

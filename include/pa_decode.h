@@ -528,7 +528,8 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  *
  * V scales are not negative: one that is, or that is not finite, makes NaN of
  * what sees its block.  V scales below 2^-60 of the largest that a call reads
- * for the same sequence and KV head may count as 2^-60 of it.
+ * for the same sequence and KV head may count as 2^-60 of it, those below
+ * 2^-126 as 0.
  *
  * A NaN code in a V row reaches every new token of the KV head's group, those
  * whose causal limit hides the row included (0 * NaN); NaN in rows past the

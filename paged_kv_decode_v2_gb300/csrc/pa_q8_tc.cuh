@@ -639,7 +639,7 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
     // A block's id, or 0 (a valid block) when out of range.
     auto valid_id = [&](int32_t id) -> int32_t { return id < 0 || id >= p.num_blocks ? 0 : id; };
 
-    float vref = 1.1754943508222875e-38f; // 2^-126, or the range's largest V scale
+    float vref = 0.f;                     // the range's largest V scale
     float ks_first = 0.f, vs_first = 0.f; // scales of block threadIdx.x
     if (warp < kMmaWarp) {
         // Q rows -> shared memory in PL parts, K-major, swizzled (16-byte chunk c of
@@ -843,7 +843,7 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
 #pragma unroll
         for (int w = 0; w < C::kSoft / 32; ++w)
             vref = fmaxf(vref, s_vref[w]);
-        const float vref_lg = fast_log2(vref);
+        const float vref_lg = fast_log2(fmaxf(vref, 1.1754943508222875e-38f)); // (2^-126)
         // Blocks that are not there get ks = 0 and any lv.
         // A V scale that is negative or not finite: weights of NaN for who sees the block.
         auto put_scales = [&](int i, float k, float v) {

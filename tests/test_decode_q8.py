@@ -241,6 +241,21 @@ def test_nan_is_not_lost(pa, lens, P, Q, what):
 
 
 @gpu
+@pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([1100, 40], 2048, 1), ([6000, 90], 64, 3), ([120, 700], 2048, 70)])
+def test_scales_of_zero(pa, lens, P, Q):
+    """K scales of 0 make the softmax uniform, V scales of 0 the output exactly 0."""
+    q = torch.randn((len(lens), Q, 8, 64)).to(BF16)
+    c = list(cu.cache8(lens, KV=2, D=64, bs=16))
+    c[2] = torch.zeros_like(c[2])
+    out, status = run(pa, q, c, 0.125, P)
+    ref, tol = cu.attend_reference(q, *c, 0.125)
+    assert status == 0 and ((out.double() - ref).abs() <= tol + cu.rounding(ref.abs() + tol, BF16)).all()
+    c[3] = torch.zeros_like(c[3])
+    out, status = run(pa, q, c, 0.125, P)
+    assert status == 0 and (out == 0).all()
+
+
+@gpu
 @pytest.mark.parametrize("dtype,G,Q", [(BF16, 2, 1), (F16, 12, 1), (BF16, 2, 30)])
 @pytest.mark.parametrize("S", [150, 256, 257])
 def test_many_sequences(pa, S, dtype, G, Q):

@@ -357,3 +357,33 @@ def test_binding_refuses_shapes(pa, q8):
             (pa.pa_kv_append_q8 if q8 else pa.pa_kv_append)(**dict(good, **{name: value}))
     torch.cuda.synchronize()
     assert torch.equal(d.key_cache.view(torch.uint8), before.view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("S,new,shape", [
+    (50, 520, dict(D=64, bs=8, KV=2, H=2, dtype=BF16, interleaved=True)),     # two heads a CTA, queries apart
+    (300, 9, dict(D=256, bs=64, KV=8, H=8, dtype=F16)),                       # the same in the widest CTAs
+    (30, 900, dict(D=128, bs=16, KV=5, H=10, dtype=BF16, rotary=64)),         # heads that two do not divide
+    (700, 3, dict(D=128, bs=32, KV=12, H=12, dtype=BF16)),
+])
+def test_q8_large_batches_equal_their_sequences(pa, S, new, shape):
+    """A batch large enough for CTAs of several heads and a launch of its own for the queries: bit for bit what one call
+    per sequence writes."""
+    counts = [(new * (b % 3) + b) % (2 * new) for b in range(S)]
+    past = [(7 * b) % 61 for b in range(S)]
+    t = cu.batch(counts, past, seed=S, padding=3, **shape)
+    whole = _run(pa, t, True)
+    d = t.cuda()
+    query = torch.full(t.query.shape, 7.0, dtype=t.query.dtype, device="cuda")
+    for b in range(S):
+        a, e = int(t.starts[b]), int(t.starts[b + 1])
+        if a < e:
+            pa.pa_kv_append_q8(d.key[a:e], d.value[a:e], d.tables[b:b + 1], d.lens[b:b + 1], d.key_cache, d.value_cache,
+                               d.k_scales, d.v_scales, cos_sin=d.cos_sin, interleaved=t.interleaved, query=d.query[a:e],
+                               query_out=query[a:e])
+    torch.cuda.synchronize()
+    assert whole[5] == 0
+    assert torch.equal(whole[0].view(torch.int16), query.cpu().view(torch.int16))
+    for got, ref in zip(whole[1:3], (d.key_cache, d.value_cache)):
+        assert torch.equal(got.view(torch.uint8), ref.cpu().view(torch.uint8))
+    assert torch.equal(whole[3], d.k_scales.cpu()) and torch.equal(whole[4], d.v_scales.cpu())

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kScanThreads) q8_offsets_kernel(const Q8CopyPa
 {
     __shared__ long long part[kScanThreads];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int per = (p.num_seqs + kScanThreads - 1) / kScanThreads;
     const int s0 = threadIdx.x * per, s1 = min(s0 + per, p.num_seqs);
     auto nblocks = [&](int s) {
@@ -84,12 +85,13 @@ __device__ __forceinline__ void widen(const uint4 &v, float scale, uint4 (&out)[
     out[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// CTAs stride over packed blocks; a thread moves 16 codes at a time.  T: the
-// type of K and, unless VH, of V.
+// CTAs stride over the K and the V of packed blocks; a thread moves 16 codes at a
+// time.  T: the type of K and, unless VH, of V.
 template <typename T, bool VH>
 __global__ void __launch_bounds__(kCopyThreads) q8_copy_kernel(const Q8CopyParams p)
 {
     __shared__ int s_id, s_rows;
+    asm volatile("griddepcontrol.wait;" ::: "memory"); // the offsets, and the flag cleared
     const int total = __ldg(p.offs + p.num_seqs);
     const int per_row = p.head_dim / 16;             // pieces of a row (a power of two)
     const int per_head = p.block_size * per_row;     // of one head of a block (a power of two)
@@ -98,7 +100,8 @@ __global__ void __launch_bounds__(kCopyThreads) q8_copy_kernel(const Q8CopyParam
     const uint4 *kc = static_cast<const uint4 *>(p.key_cache);
     const uint4 *vc = static_cast<const uint4 *>(p.value_cache);
     bool odd = false;
-    for (int q = blockIdx.x; q < total; q += gridDim.x) {
+    for (long long item = blockIdx.x; item < 2LL * total; item += gridDim.x) {
+        const int q = (int)(item >> 1), which = (int)(item & 1);
         __syncthreads();
         if (threadIdx.x == 0) {
             int lo = 0, hi = p.num_seqs - 1; // the last s with offs[s] <= q
@@ -112,54 +115,54 @@ __global__ void __launch_bounds__(kCopyThreads) q8_copy_kernel(const Q8CopyParam
             const int j = q - __ldg(p.offs + lo);
             int id = __ldg(p.block_tables + (size_t)lo * p.max_blocks + j);
             if (id < 0 || id >= p.num_blocks) {
-                set_status(p.status, PA_STATUS_BAD_BLOCK_ID);
+                if (which == 0)
+                    set_status(p.status, PA_STATUS_BAD_BLOCK_ID);
                 id = 0; // read a valid block instead of memory outside the cache
             }
             s_id = id;
             s_rows = min(p.block_size,
                          clamp_len(__ldg(p.seq_lens + lo), p.seq_len_cap) - j * p.block_size);
-            p.table[(size_t)lo * p.table_width + j] = q;
+            if (which == 0)
+                p.table[(size_t)lo * p.table_width + j] = q;
         }
         __syncthreads();
         const int id = s_id, rows = s_rows;
         const size_t src = (size_t)id * pieces;
-        for (int which = 0; which < 2; ++which) {
-            const uint4 *in = (which ? vc : kc) + src;
-            const float *scales = (which ? p.v_scales : p.k_scales) + (size_t)id * p.num_kv_heads;
-            uint4 *out = static_cast<uint4 *>(which ? p.v_copy : p.k_copy);
-            for (int base = threadIdx.x; base < pieces; base += kCopyRounds * kCopyThreads) {
-                uint4 x[kCopyRounds];
+        const uint4 *in = (which ? vc : kc) + src;
+        const float *scales = (which ? p.v_scales : p.k_scales) + (size_t)id * p.num_kv_heads;
+        uint4 *out = static_cast<uint4 *>(which ? p.v_copy : p.k_copy);
+        for (int base = threadIdx.x; base < pieces; base += kCopyRounds * kCopyThreads) {
+            uint4 x[kCopyRounds];
 #pragma unroll
-                for (int u = 0; u < kCopyRounds; ++u) {
-                    const int i = base + u * kCopyThreads;
-                    const bool in_row = i < pieces && ((i & (per_head - 1)) >> lg_row) < rows;
-                    x[u] = in_row ? __ldg(in + i) : make_uint4(0u, 0u, 0u, 0u);
-                }
+            for (int u = 0; u < kCopyRounds; ++u) {
+                const int i = base + u * kCopyThreads;
+                const bool in_row = i < pieces && ((i & (per_head - 1)) >> lg_row) < rows;
+                x[u] = in_row ? __ldg(in + i) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-                for (int u = 0; u < kCopyRounds; ++u) {
-                    const int i = base + u * kCopyThreads;
-                    if (i >= pieces)
-                        continue;
-                    const int h = i >> lg_head;
-                    float s = __ldg(scales + h);
-                    if (which && !(s >= 0.f && s <= 3.4028234663852886e38f))
-                        s = NAN; // as in the 8-bit kernel
-                    // Codes but for their signs.
-                    const uint32_t any = (x[u].x | x[u].y | x[u].z | x[u].w) & 0x7f7f7f7fu;
-                    const bool half_out = VH ? which == 1 : sizeof(T) == 2 && !Elem<T>::kSplitP;
-                    if (half_out && any != 0u && !(s >= 3.0517578125e-5f && s <= 128.f))
-                        odd = true;
-                    uint4 y[2];
-                    if (VH && which == 1)
-                        widen<__half>(x[u], s, y);
-                    else
-                        widen<T>(x[u], s, y);
-                    const size_t at = VH && which == 1
-                                          ? ((size_t)h * p.copy_blocks + q) * per_head + (i & (per_head - 1))
-                                          : (size_t)q * pieces + i;
-                    out[2 * at] = y[0];
-                    out[2 * at + 1] = y[1];
-                }
+            for (int u = 0; u < kCopyRounds; ++u) {
+                const int i = base + u * kCopyThreads;
+                if (i >= pieces)
+                    continue;
+                const int h = i >> lg_head;
+                float s = __ldg(scales + h);
+                if (which && !(s >= 0.f && s <= 3.4028234663852886e38f))
+                    s = NAN; // as in the 8-bit kernel
+                // Codes but for their signs.
+                const uint32_t any = (x[u].x | x[u].y | x[u].z | x[u].w) & 0x7f7f7f7fu;
+                const bool half_out = VH ? which == 1 : sizeof(T) == 2 && !Elem<T>::kSplitP;
+                if (half_out && any != 0u && !(s >= 3.0517578125e-5f && s <= 128.f))
+                    odd = true;
+                uint4 y[2];
+                if (VH && which == 1)
+                    widen<__half>(x[u], s, y);
+                else
+                    widen<T>(x[u], s, y);
+                const size_t at = VH && which == 1
+                                      ? ((size_t)h * p.copy_blocks + q) * per_head + (i & (per_head - 1))
+                                      : (size_t)q * pieces + i;
+                out[2 * at] = y[0];
+                out[2 * at + 1] = y[1];
             }
         }
     }
@@ -184,16 +187,14 @@ cudaError_t launch_q8_copy(int dtype, bool v_half, const Q8CopyParams &p, int nu
     cudaError_t e = cudaLaunchKernelEx(&cfg, q8_offsets_kernel, p);
     if (e != cudaSuccess)
         return e;
-    const long long most = (long long)p.num_seqs * ((p.seq_len_cap + p.block_size - 1) / p.block_size);
+    const long long most = 2LL * p.num_seqs * ((p.seq_len_cap + p.block_size - 1) / p.block_size);
     const long long slots = 8LL * num_sms;
     const unsigned grid = (unsigned)(most < slots ? (most > 0 ? most : 1) : slots);
-    if (v_half)
-        q8_copy_kernel<__nv_bfloat16, true><<<grid, kCopyThreads, 0, stream>>>(p);
-    else if (dtype == PA_BF16)
-        q8_copy_kernel<__nv_bfloat16, false><<<grid, kCopyThreads, 0, stream>>>(p);
-    else
-        q8_copy_kernel<__half, false><<<grid, kCopyThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kCopyThreads);
+    return v_half              ? cudaLaunchKernelEx(&cfg, q8_copy_kernel<__nv_bfloat16, true>, p)
+           : dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, q8_copy_kernel<__nv_bfloat16, false>, p)
+                              : cudaLaunchKernelEx(&cfg, q8_copy_kernel<__half, false>, p);
 }
 
 } // namespace pa

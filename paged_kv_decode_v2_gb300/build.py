@@ -57,7 +57,7 @@ def _compile_bind(force: bool) -> str:
     obj = os.path.join(BUILD, f"pa_bind-{torch.__version__}.o")
     if force or _stale(obj, [src] + _headers()):
         inc = os.path.join(os.path.dirname(torch.__file__), "include")
-        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
         _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
               "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),

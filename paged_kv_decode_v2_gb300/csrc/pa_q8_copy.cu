@@ -18,8 +18,9 @@
 // scale outside [2^-15, 2^7], beside which a code's values run from 2^-24 to
 // 57344 -- sets the flag: the call then runs the 8-bit kernel instead.
 //
-// Bound by its bytes: one read of the codes, two bytes written for each; 25 us for
-// 36 MB of codes (63% of the measured copy bandwidth), beside 293 of attention.
+// Bound by its bytes and the chain that finds a block: one read of the codes, two bytes
+// written for each; 24 us alone for 36 MB of codes (66% of the measured copy
+// bandwidth), before 293 of attention.
 #include <cuda_fp8.h>
 
 #include "pa_device.cuh"

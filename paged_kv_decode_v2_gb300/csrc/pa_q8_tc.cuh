@@ -1223,7 +1223,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
 }
 
 // V1 after the 16-bit copy's attention: runs only if the copy's flag is up, mostly not,
-// so a CTA per SM takes all the work (two chunks of 1024 new tokens: 308 us, 314 with a
+// so a CTA per SM takes all the work (two chunks of 1024 new tokens then 308 us, 314 with a
 // CTA for each unit, the wide CTAs leaving wave by wave; 31 of 390 on 3 heads 263, 282).
 template <int D, int NR, int PL>
 __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)

@@ -419,6 +419,7 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
         // sequence (V1: each sequence) in 32 classes of size, so that no long one is
         // left for the end.  Every CTA sorts: thread = sequence.
         constexpr int kWarps = C::kThreads / 32;
+        static_assert(C::kThreads >= kQ8Sorted, "a thread holds one sequence");
         __shared__ int s_count[kWarps][32]; // sequences of each class, by warp
         __shared__ int s_whole[kWarps];     // whole partitions
         __shared__ int s_pick[3];
@@ -594,13 +595,13 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
         const uint32_t dst = p_ring + (uint32_t)s * C::kTile + p_first * bs * C::kRB;
         if (lane == 0)
             mbar_arrive_expect_tx(bar, (uint32_t)nb * bs * D);
+        const int row = (id * p.num_kv_heads + kv) << sh; // (all rows number less than 2^31)
         for (int i = 0; i < nb; ++i) {
-            const int32_t phys = __shfl_sync(0xffffffffu, id, i);
+            const int at = __shfl_sync(0xffffffffu, row, i);
             if (lane == 0) {
-                const int row = (int)(((long long)phys * p.num_kv_heads + kv) * bs);
 #pragma unroll
                 for (int sl = 0; sl < C::kSlices; ++sl)
-                    tma_load_3d(dst + sl * C::kSlice + i * bs * C::kRB, p_map, 0, sl, row, bar, policy);
+                    tma_load_3d(dst + sl * C::kSlice + i * bs * C::kRB, p_map, 0, sl, at, bar, policy);
             }
         }
     };

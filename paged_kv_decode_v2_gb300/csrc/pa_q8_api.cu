@@ -273,7 +273,13 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
     Q8Cut cut = {0, 1, 0};
     if (tiles <= 1)
         return cut;
-    const long long ways = std::max(1LL, std::min(std::min((long long)kQ8Ways, tiles), sms / groups));
+    // Clusters lie inside the GPU's groups of SMs, whose remainders stay empty: of 152
+    // SMs with a CTA each, 15 clusters of 8 run at a time, 36 of 4, 76 of 2 (of 3, 5, 6
+    // and 7: 46, 28, 23, 15).  48 groups of 4768 tokens (64 rows, fp16) took two waves
+    // and 72 us as clusters of 3, 44 as partitions.
+    static_assert(kQ8Ways == 8, "the sizes tried");
+    const long long most = 8 * groups <= sms * 3 / 4 ? 8 : 4 * groups <= sms * 9 / 10 ? 4 : 2 * groups <= sms ? 2 : 1;
+    const long long ways = std::min(most, tiles);
     const long long per = (tiles + ways - 1) / ways;
     cut.ways = (int)((tiles + per - 1) / per);
     cut.per = (int)std::min(per * kQ8Tok, (long long)INT32_MAX);
@@ -302,6 +308,10 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
 // sequences of 9000 tokens 128 rows 56 / 52, 256 rows 67 / 82, 1024 rows 116 / 259;
 // 16 of 2000 86 / 75, 99 / 146, 247 / 489.
 constexpr int kQ8CopyRows = 256;
+// And from this many tiles of 128 tokens by 64 rows on: one sequence of 4000 tokens, 256
+// rows (992 tiles) 32 / 27, 512 rows (1984) 42 / 40, 2048 rows (7936) 60 / 114; 20,000
+// tokens on one KV head, 512 rows (1256) 36 / 30; 4 of 600, 512 rows (1280) 31 / 36.
+constexpr long long kQ8CopyTiles = 2048;
 
 struct CopyPlan {
     bool v_half;   // V in binary16 beside a bf16 K, for the two-tile kernel
@@ -503,7 +513,8 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
     L.block_size = block_size;
     L.mode = part == 0 ? kQ8V1 : kQ8V2;
 
-    if (work_ok && p.cols >= kQ8CopyRows) {
+    if (work_ok && p.cols >= kQ8CopyRows &&
+        (long long)num_seqs * num_kv_heads * ((p.cols + 63) / 64) * ((cap + 127LL) / 128) >= kQ8CopyTiles) {
         Q8CopyParams c = {};
         CopyPlan plan;
         if (plan_copy(plan, c, p, partition_size, num_seqs, block_size, head_dim)) {

@@ -187,6 +187,17 @@ def test_many_rows(pa, D, bs, KV, dtype):
 def test_many_rows_that_no_copy_can_hold(pa, D, bs, dtype):
     """More units of the 8-bit kernel than the GPU has SMs, after the copy's attention."""
     check(pa, [320, 0, 301, 40], Q=300, G=4, KV=3, D=D, bs=bs, dtype=dtype, P=128, scales="wild")
+    check(pa, [1300, 0, 301, 40], Q=300, G=4, KV=3, D=D, bs=bs, dtype=dtype, P=128, scales="wild")
+
+
+@gpu
+@pytest.mark.parametrize("D,bs,dtype", [(64, 16, F16), (64, 8, BF16), (128, 32, BF16), (128, 16, F16), (256, 64, BF16)])
+@pytest.mark.parametrize("scales", ["blocks", "any", "zero"])
+def test_many_rows_of_long_sequences(pa, D, bs, dtype, scales):
+    """Enough of them for the 16-bit copy: stale NaN rows, scales that are no powers of two, a sequence below q_len."""
+    held = cu.HALF_STEP[dtype] if scales == "any" else 0.0
+    check(pa, [1800, 33, 0, 290, 700], Q=300, G=4, KV=2, D=D, bs=bs, dtype=dtype, P=128, scales=scales, held=held,
+          poison=scales == "blocks")
 
 
 @gpu
@@ -216,7 +227,7 @@ def test_hint_and_long_cache(pa):
 @gpu
 @pytest.mark.parametrize("what", ["k code", "v code", "k scale", "v scale", "v scale < 0", "v scale inf"])
 @pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([300, 90], 64, 2), ([1100, 40], 2048, 1), ([6000, 90], 64, 3),
-                                      ([500] * 160, 512, 1), ([120, 700], 2048, 70)])
+                                      ([500] * 160, 512, 1), ([120, 700], 2048, 70), ([3600, 400], 64, 300)])
 def test_nan_is_not_lost(pa, lens, P, Q, what):
     """V1 on one CTA and on a cluster, V2, sorted units, the 16-bit copy: NaN reaches what sees it, and nothing else."""
     kc, vc, ks, vs, tables, lens = c = cu.cache8(lens, KV=2, D=64, bs=16)
@@ -241,7 +252,7 @@ def test_nan_is_not_lost(pa, lens, P, Q, what):
 
 
 @gpu
-@pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([1100, 40], 2048, 1), ([6000, 90], 64, 3), ([120, 700], 2048, 70)])
+@pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([1100, 40], 2048, 1), ([6000, 90], 64, 3), ([120, 700], 2048, 70), ([3600, 400], 64, 300)])
 def test_scales_of_zero(pa, lens, P, Q):
     """K scales of 0 make the softmax uniform, V scales of 0 the output exactly 0."""
     q = torch.randn((len(lens), Q, 8, 64)).to(BF16)

@@ -517,8 +517,8 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  * partition_size).  The intermediates must be valid whenever V2 can be chosen;
  * their contents after the call are unspecified.
  *
- * From 256 query rows (q_len * G) per KV head and some work on, when tmp_output
- * has room for it, the call first makes a 16-bit copy of the blocks that it reads there (in
+ * From 256 query rows (q_len * G) per KV head and 2048 tiles (of 128 tokens up
+ * to max_seq_len by 64 rows) on, when tmp_output has room for it, the call first makes a 16-bit copy of the blocks that it reads there (in
  * the query's type, K and V of num_seqs * ceil(max_seq_len / block_size)
  * blocks, beside the partials) and runs pa_decode_mq's kernels over that:
  * values are then rounded to 16 bits, which loses nothing under scales that

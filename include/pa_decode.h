@@ -520,11 +520,11 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  * From 256 query rows (q_len * G) per KV head and 2048 tiles (of 128 tokens up
  * to max_seq_len by 64 rows) on, when tmp_output has room for it, the call first makes a 16-bit copy of the blocks that it reads there (in
  * the query's type, K and V of num_seqs * ceil(max_seq_len / block_size)
- * blocks, beside the partials) and runs pa_decode_mq's kernels over that:
- * values are then rounded to 16 bits, which loses nothing under scales that
- * are powers of two.  Values that binary16 cannot hold (a nonzero code under
- * a scale outside [2^-15, 2^7]) are found on the device and the 8-bit kernel
- * runs instead.
+ * blocks, beside the partials) and runs pa_decode_mq's kernels over that.
+ * The copy holds what it stands for exactly, under scales that are powers of
+ * two, as pa_kv_append_q8 writes them, in the type's range (binary16 [2^-15,
+ * 2^7], bfloat16 [2^-117, 2^119], or 0).  A nonzero code under any other scale
+ * is found on the device, and the 8-bit kernel runs instead.
  *
  * V scales are not negative: one that is, or that is not finite, makes NaN of
  * what sees its block.  V scales below 2^-60 of the largest that a call reads

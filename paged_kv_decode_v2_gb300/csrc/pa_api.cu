@@ -526,7 +526,7 @@ int v2_phase1_impl(const void *query, const void *key_cache, const void *value_c
                    int dtype, float *tmp_output, float *exp_sums, float *max_logits,
                    int max_num_partitions, int32_t *status, cudaStream_t stream, int *cap_out,
                    void *fused_out = nullptr, int32_t *counters = nullptr,
-                   const VhCopy *vh = nullptr)
+                   const VhCopy *vh = nullptr, const int32_t *skip_if = nullptr)
 {
     int rc = check_shape(query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                          num_heads, num_kv_heads, head_dim, num_blocks, block_size,
@@ -558,6 +558,7 @@ int v2_phase1_impl(const void *query, const void *key_cache, const void *value_c
                     max_num_partitions, fused_out, status, counters, vh);
     if (rc)
         return rc;
+    L.p.skip_if = skip_if;
     return prepare_and_launch_attn(L, stream);
 }
 
@@ -824,7 +825,8 @@ int v2_mq_impl(const void *query, const void *key_cache, const void *value_cache
                int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size,
                int max_blocks_per_seq, int max_seq_len_hint, float scale, int partition_size,
                int dtype, void *out, float *tmp_output, float *exp_sums, float *max_logits,
-               int max_num_partitions, int32_t *status, cudaStream_t stream, const VhCopy *vh)
+               int max_num_partitions, int32_t *status, cudaStream_t stream, const VhCopy *vh,
+               const int32_t *skip_if = nullptr)
 {
     if (!out || !aligned(out, 4))
         return PA_ERR_INVALID_ARG;
@@ -833,7 +835,7 @@ int v2_mq_impl(const void *query, const void *key_cache, const void *value_cache
                             num_heads, num_kv_heads, head_dim, num_blocks, block_size,
                             max_blocks_per_seq, max_seq_len_hint, scale, partition_size, dtype,
                             tmp_output, exp_sums, max_logits, max_num_partitions, status, stream,
-                            &cap, nullptr, nullptr, vh);
+                            &cap, nullptr, nullptr, vh, skip_if);
     if (rc)
         return rc;
     return v2_phase2_impl(seq_lens, num_seqs, q_len, num_heads, head_dim, cap, partition_size,
@@ -846,7 +848,8 @@ int v1_mq_impl(const void *query, const void *key_cache, const void *value_cache
                const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int q_len,
                int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size,
                int max_blocks_per_seq, int max_seq_len_hint, float scale, int dtype, void *out,
-               int32_t *status, cudaStream_t stream, const VhCopy *vh)
+               int32_t *status, cudaStream_t stream, const VhCopy *vh,
+               const int32_t *skip_if = nullptr)
 {
     int rc = check_shape(query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                          num_heads, num_kv_heads, head_dim, num_blocks, block_size,
@@ -866,6 +869,7 @@ int v1_mq_impl(const void *query, const void *key_cache, const void *value_cache
                     nullptr, vh);
     if (rc)
         return rc;
+    L.p.skip_if = skip_if;
     return prepare_and_launch_attn(L, stream);
 }
 
@@ -934,16 +938,17 @@ int host_mq_over_copy(const void *query, const void *k, const void *v, bool v_ha
 {
     VhCopy vh{const_cast<void *>(v), const_cast<int32_t *>(flag), offs, num_blocks};
     const VhCopy *vhp = v_half ? &vh : nullptr;
-    // With V's binary16 copy the bf16 V cache is read only when its flag is set,
-    // and the caller then replaces the result: any valid array will do.
+    // With V's binary16 copy the bf16 V cache would be read only when its flag is set,
+    // where the kernel leaves at once (or, mma.sync by pa_set_rows_kernel, computes
+    // what the caller then replaces): any valid array will do.
     const void *v_cache = v_half ? k : v;
     if (part == 0)
         return v1_mq_impl(query, k, v_cache, table, seq_lens, num_seqs, q_len, num_heads,
                           num_kv_heads, head_dim, num_blocks, block_size, table_width, cap, scale,
-                          dtype, out, status, stream, vhp);
+                          dtype, out, status, stream, vhp, flag);
     return v2_mq_impl(query, k, v_cache, table, seq_lens, num_seqs, q_len, num_heads, num_kv_heads,
                       head_dim, num_blocks, block_size, table_width, cap, scale, part, dtype, out,
-                      tmp_output, exp_sums, max_logits, np, status, stream, vhp);
+                      tmp_output, exp_sums, max_logits, np, status, stream, vhp, flag);
 }
 
 int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, int head_dim,

@@ -51,6 +51,7 @@ struct AttnParams {
     const int32_t *vh_flag;      // binary16 copy of V: its flag, 0 when the copy holds V
     const int32_t *vh_offs;      // binary16 copy of V: each sequence's first block in it
     int vh_blocks;               // and the blocks one KV head's part of it holds
+    const int32_t *skip_if;      // tcgen05 kernels: leave at once if this word is not 0; or null
     int32_t *status;
 };
 

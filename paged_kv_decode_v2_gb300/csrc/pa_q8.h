@@ -28,7 +28,8 @@ int host_merge(const int32_t *seq_lens, int num_seqs, int q_len, int num_heads, 
 
 // The 16-bit multi-query attention over copies of K and V (partials at a stride
 // of np partitions of `part` tokens, V1 when part is 0), bf16 with V's binary16
-// copy as pa_decode_mq uses it (v_half; else v is a cache like k).
+// copy as pa_decode_mq uses it (v_half; else v is a cache like k).  Where *flag is
+// up the attention does nothing, and what `out` holds then is unspecified.
 int host_mq_over_copy(const void *query, const void *k, const void *v, bool v_half,
                       const int32_t *flag, const int32_t *offs, const int32_t *table,
                       const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,

@@ -314,9 +314,8 @@ constexpr int kQ8CopyRows = 256;
 constexpr long long kQ8CopyTiles = 2048;
 
 struct CopyPlan {
-    bool v_half;   // V in binary16 beside a bf16 K, for the two-tile kernel
-    bool may_flag; // some of the copy is binary16
-    int part, np;  // pa_decode_mq's choice
+    bool v_half;  // V in binary16 beside a bf16 K, for the two-tile kernel
+    int part, np; // pa_decode_mq's choice
 };
 
 // Lays the copy out in tmp_output behind the partials the 16-bit call writes
@@ -333,7 +332,6 @@ bool plan_copy(CopyPlan &plan, Q8CopyParams &c, const Q8Params &p, int partition
     if (plan.np > p.max_num_partitions)
         return false;
     plan.v_half = p.dtype == PA_BF16 && host_two_tiles(p.cols, head_dim, p.seq_len_cap);
-    plan.may_flag = plan.v_half || p.dtype == PA_F16;
     const long long width = ((long long)p.seq_len_cap + block_size - 1) / block_size;
     const long long blocks = width * num_seqs;
     const long long rows = (long long)p.num_kv_heads * block_size;
@@ -526,10 +524,10 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
                                    seq_lens, num_seqs, q_len, num_heads, num_kv_heads, head_dim,
                                    c.copy_blocks, block_size, c.table_width, cap, scale, plan.part,
                                    plan.np, dtype, out, tmp_output, exp_sums, max_logits, status, st);
-            if (rc || !plan.may_flag)
+            if (rc)
                 return rc;
-            // Values that binary16 cannot hold: the 8-bit kernel runs after all (V1,
-            // which needs no intermediates, over the result above).
+            // Values that 16 bits do not hold exactly: the kernels above have left at once,
+            // and the 8-bit one runs after all (V1, which needs no intermediates).
             p.only_if = c.flag;
             L.mode = kQ8If;
             p.ways = 1;

@@ -12,11 +12,13 @@
 //   V  the same for binary16 queries; for bf16 ones binary16 in the layout
 //      [KV][copy_blocks][block_size][D] that the two-tile kernel's binary16
 //      P.V reads.
-// value = code * scale, rounded once: exact for scales that are powers of two
-// as the append writes them, off by at most half a step of the 16-bit type
-// otherwise.  A value that binary16 cannot hold so -- a nonzero code under a
-// scale outside [2^-15, 2^7], beside which a code's values run from 2^-24 to
-// 57344 -- sets the flag: the call then runs the 8-bit kernel instead.
+// value = code * scale, exactly: the scales that the append writes are powers of two, and
+// what the 16-bit types hold under them is what the 8-bit kernel multiplies.  A nonzero
+// code under any other scale -- one that is no power of two, or so large or small that
+// the type does not hold every code's value under it (see exact_under) -- sets the flag:
+// the 16-bit attention behind then returns at once and the call runs the 8-bit kernel,
+// so that a result's precision depends neither on the number of rows nor on the
+// workspace.
 //
 // Bound by its bytes and the chain that finds a block: one read of the codes, two bytes
 // written for each; 24 us alone for 36 MB of codes (66% of the measured copy
@@ -68,6 +70,17 @@ __global__ void __launch_bounds__(kScanThreads) q8_offsets_kernel(const Q8CopyPa
         p.offs[p.num_seqs] = (int32_t)part[threadIdx.x];
         *p.flag = 0;
     }
+}
+
+// Whether T holds every code times s: e4m3 has 4 significant bits and values from 2^-9 to
+// 448 = 1.75 * 2^8.  binary16 holds multiples of 2^-24 and up to 65504; bf16's range is
+// kept to its normal values, from 2^-126.
+template <typename T>
+__device__ __forceinline__ bool exact_under(float s)
+{
+    const float lo = Elem<T>::kSplitP ? 6.018531076210112e-36f : 3.0517578125e-5f; // 2^-117, 2^-15
+    const float hi = Elem<T>::kSplitP ? 6.646139978924579e35f : 128.f;             // 2^119, 2^7
+    return s == 0.f || ((__float_as_uint(s) & 0x7fffffu) == 0u && s >= lo && s <= hi);
 }
 
 template <typename T>
@@ -151,8 +164,7 @@ __global__ void __launch_bounds__(kCopyThreads) q8_copy_kernel(const Q8CopyParam
                     s = NAN; // as in the 8-bit kernel
                 // Codes but for their signs.
                 const uint32_t any = (x[u].x | x[u].y | x[u].z | x[u].w) & 0x7f7f7f7fu;
-                const bool half_out = VH ? which == 1 : sizeof(T) == 2 && !Elem<T>::kSplitP;
-                if (half_out && any != 0u && !(s >= 3.0517578125e-5f && s <= 128.f))
+                if (any != 0u && !(VH && which == 1 ? exact_under<__half>(s) : exact_under<T>(s)))
                     odd = true;
                 uint4 y[2];
                 if (VH && which == 1)

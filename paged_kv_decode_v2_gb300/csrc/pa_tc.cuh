@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kTcThreads, D <= 128 ? 2 : 1)
     // the previous grid in the stream has completed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (p.skip_if && __ldcg(p.skip_if) != 0)
+        return;
 
     int L = __ldg(&p.seq_lens[b]);
     if (L < 0 || L > p.seq_len_cap) {

@@ -613,6 +613,8 @@ __global__ void __launch_bounds__(kTc2Threads)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (p.skip_if && __ldcg(p.skip_if) != 0)
+        return;
     if constexpr (VH) {
         if (__ldcg(p.vh_flag) == 0)
             tc2_body<T, D, BS, V1, true>(tmap_k, tmap_v, tmap_vh, p);

@@ -556,9 +556,10 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : MANY ? 3 : 4)
     const int warps = blockDim.x >> 5;
     for (int kv = kv0; kv < kv1; ++kv) {
         const size_t slot = slot0 + kv;
-        // Rows below new_lo hold earlier tokens: their scale is a floor.
-        const float old_k = new_lo > 0 ? __ldg(p.k_scales + slot) : 0.f;
-        const float old_v = new_lo > 0 ? __ldg(p.v_scales + slot) : 0.f;
+        // Rows below new_lo hold earlier tokens: their scale is a floor.  Plain loads, which
+        // stay before the barrier behind which thread 0 writes the slot.
+        const float old_k = new_lo > 0 ? p.k_scales[slot] : 0.f;
+        const float old_v = new_lo > 0 ? p.v_scales[slot] : 0.f;
         float a[8], d[8];
         unpack8<T>(k0, a);
         unpack8<T>(k1, d);

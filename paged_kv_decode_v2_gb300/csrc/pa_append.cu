@@ -339,6 +339,13 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], float f)
                       to_e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
 }
 
+__device__ __forceinline__ void divide8(float (&x)[8], float s)
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        x[k] = __fdiv_rn(x[k], s);
+}
+
 __device__ __forceinline__ void from_e4m3x8(uint2 v, float (&x)[8])
 {
     const uint32_t w[2] = {v.x, v.y};
@@ -613,8 +620,16 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : MANY ? 3 : 4)
         uint2 *kd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.key_cache) + at);
         uint2 *vd = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) + at);
         if (is_new) {
-            // x / s is x times an exact power of two for the scales this writes.
-            const float fk = 1.f / sk, fv = 1.f / sv;
+            // x / s is x times an exact power of two for the scales this writes; under an
+            // old one that is none, the reciprocal's rounding would decide ties.
+            float fk = 1.f / sk, fv = 1.f / sv;
+            if (((__float_as_uint(sk) | __float_as_uint(sv)) & 0x7fffffu) != 0u) {
+                divide8(a, sk);
+                divide8(d, sk);
+                divide8(x, sv);
+                divide8(y, sv);
+                fk = fv = 1.f;
+            }
             kd[rot.c0] = to_e4m3x8(a, fk);
             kd[rot.c1] = to_e4m3x8(d, fk);
             const uint2 e = to_e4m3x8(x, fv), f = to_e4m3x8(y, fv);

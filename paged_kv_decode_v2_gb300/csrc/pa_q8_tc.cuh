@@ -75,7 +75,8 @@
 namespace pa {
 
 constexpr float kQ8Ln2 = 0.69314718055994531f;
-constexpr float kQ8NoMax = -1e30f; // M before a row has seen a token
+// M before a row has seen a token: the lowest finite value, so that any score moves it.
+constexpr float kQ8NoMax = -3.4028234663852886e38f;
 constexpr float kQ8Grow = 4.f;     // weights stay <= 2^4,
 constexpr float kQ8Unit = 11.f;    // stored times 2^11: <= 2^15 (e5m2's largest is 1.75 * 2^15)
 constexpr float kQ8Floor = -60.f;  // of log2(vs / r)

@@ -79,3 +79,32 @@ def test_scales_are_kept_whatever_the_rows_and_the_workspace(pa, D, dtype, Q, G)
         assert status == 0
         out = out[:, -2:].double()
         assert ((out - ref).abs() <= tol + cu.rounding(ref.abs() + tol, dtype)).all(), float((out - ref).abs().max())
+
+
+# ---------------------------------------------------------------- scores of any finite size
+
+
+@gpu
+@pytest.mark.parametrize("lens,P,Q", [([130], 2048, 1), ([1100, 40], 2048, 1), ([6000, 300], 64, 3), ([300, 700], 2048, 70)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_very_negative_scores(pa, lens, P, Q, dtype):
+    """Every score below -1e30: the softmax is all on the largest of them, as for any others."""
+    D, bs = 64, 16
+    n = [-(-x // bs) for x in lens]
+    tables = torch.full((len(lens), max(n)), -1, dtype=torch.int32)
+    at = 0
+    for b, x in enumerate(n):
+        tables[b, :x] = torch.arange(at, at + x, dtype=torch.int32)
+        at += x
+    g = torch.Generator().manual_seed(2)
+    k = torch.ones(at, 1, bs, D)
+    v = torch.randint(-8, 9, (at, 1, bs, D), generator=g).float()
+    q = torch.full((len(lens), Q, 4, D), -1.0, dtype=dtype)
+    best = [5, 17]
+    for b in range(len(lens)):
+        k[tables[b, best[b] // bs], 0, best[b] % bs] = 0.5
+    c = (k.to(E4M3), v.to(E4M3), torch.full((at, 1), 2.0 ** 104), torch.ones(at, 1), tables, torch.tensor(lens, dtype=torch.int32))
+    out, status = run(pa, q, c, 0.125, P)
+    assert status == 0
+    for b in range(len(lens)):
+        assert (out[b].float() == v[tables[b, best[b] // bs], 0, best[b] % bs]).all()

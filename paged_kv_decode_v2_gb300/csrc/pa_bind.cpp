@@ -244,6 +244,8 @@ int append(PyObject *const *a, bool q8)
     if (cos_sin) {
         if (cos_sin->scalar_type() != at::kFloat || cos_sin->dim() != 2 || !cos_sin->is_contiguous())
             bad_value("cos_sin must be a contiguous float32 [max_positions, rotary_dim]");
+        if (cos_sin->numel() == 0) // (it has no address, which would mean no rotation)
+            bad_value("cos_sin must not be empty");
         positions = to_int(cos_sin->size(0));
         rotary = to_int(cos_sin->size(1));
     }

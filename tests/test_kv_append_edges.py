@@ -58,6 +58,20 @@ def test_codes_under_a_scale_that_is_no_power_of_two(pa, dtype, scale):
         assert torch.equal(got, want), int((got != want).sum())
 
 
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+def test_a_table_of_no_positions_is_refused(pa, q8):
+    """(an empty tensor has no address, and a call without a table does not rotate)"""
+    d = cu.batch([2, 1], [3, 0], q8=q8).cuda()
+    args = (d.key, d.value, d.tables, d.lens, d.key_cache, d.value_cache) + ((d.k_scales, d.v_scales) if q8 else ())
+    before = d.key_cache.clone()
+    for empty in (d.cos_sin[:0], d.cos_sin[:, :0].contiguous()):
+        with pytest.raises(ValueError):
+            (pa.pa_kv_append_q8 if q8 else pa.pa_kv_append)(*args, cos_sin=empty, token_starts=d.starts)
+    torch.cuda.synchronize()
+    assert torch.equal(d.key_cache.view(torch.uint8), before.view(torch.uint8))
+
+
 def test_what_the_append_writes_is_not_loaded_as_constant(cuda_lib):
     """__ldg promises that its array stays as it is during the launch: none that the appends write is loaded so."""
     csrc = os.path.join(os.path.dirname(cuda_lib.LIB_PATH), "csrc")

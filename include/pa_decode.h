@@ -277,8 +277,9 @@ PA_API int pa_decode_mq_choose(int num_seqs, int q_len, int num_heads, int num_k
 /*
  * The partition size pa_decode_mq runs V2 with for these sizes: at least
  * partition_size (the intermediates sized for partition_size therefore
- * always suffice), or 0 when it runs V1.  Negative PA_ERR_* code for invalid arguments.  Host
- * only.  No counterpart in the method's description.
+ * always suffice), or 0 when it runs V1.  Negative PA_ERR_* code for invalid arguments and
+ * for sizes that pa_decode_mq does not support.  Host only.  No counterpart in the method's
+ * description.
  */
 PA_API int pa_decode_mq_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
                                   int head_dim, int max_seq_len, int partition_size);
@@ -548,7 +549,7 @@ PA_API int pa_decode_q8(const void *query, const void *key_cache, const void *va
  * The partition size pa_decode_q8 runs V2 with for these sizes on the current
  * device: at least partition_size (intermediates sized for partition_size
  * always suffice), or 0 when it runs V1.  Negative PA_ERR_* code for invalid
- * arguments.  Host only.
+ * arguments and for sizes that pa_decode_q8 does not support.  Host only.
  */
 PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
                                   int head_dim, int max_seq_len, int partition_size);

@@ -888,6 +888,19 @@ int host_device(int *dev, int *sms)
 
 int host_check_q_len(int num_seqs, int q_len) { return check_q_len(num_seqs, q_len); }
 
+// (The limits of the calls that the queries are about; within them no product of
+// sizes that the choice forms overflows.)
+int host_check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                      int max_seq_len, int partition_size)
+{
+    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_heads / num_kv_heads > kMaxGQA || num_seqs > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    return check_q_len(num_seqs, q_len);
+}
+
 int host_seq_cap(int max_blocks_per_seq, int block_size, int hint)
 {
     return seq_cap(max_blocks_per_seq, block_size, hint);
@@ -1093,9 +1106,10 @@ PA_API int pa_decode_choose(int num_seqs, int num_kv_heads, int max_seq_len, int
 PA_API int pa_decode_mq_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads,
                                int head_dim, int max_seq_len, int partition_size)
 {
-    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
-        return -PA_ERR_INVALID_ARG;
+    const int rc = host_check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                     partition_size);
+    if (rc)
+        return -rc;
     int dev;
     if (current_device(&dev))
         return -PA_ERR_CUDA;
@@ -1110,9 +1124,10 @@ PA_API int pa_decode_mq_choose(int num_seqs, int q_len, int num_heads, int num_k
 PA_API int pa_decode_mq_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
                                   int head_dim, int max_seq_len, int partition_size)
 {
-    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
-        return -PA_ERR_INVALID_ARG;
+    const int rc = host_check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                     partition_size);
+    if (rc)
+        return -rc;
     int dev;
     if (current_device(&dev))
         return -PA_ERR_CUDA;

@@ -15,6 +15,9 @@ namespace pa {
 // Host helpers of pa_api.cu that the cache operators share with the 16-bit path.
 int host_device(int *dev, int *sms);             // current device and its SM count
 int host_check_q_len(int num_seqs, int q_len);
+// Arguments of the queries for a call's variant and partition size.
+int host_check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
+                      int max_seq_len, int partition_size);
 int host_seq_cap(int max_blocks_per_seq, int block_size, int hint);
 bool host_aligned(const void *p, uintptr_t a);
 int host_encode_tiled(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base,

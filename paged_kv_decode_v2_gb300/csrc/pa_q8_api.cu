@@ -369,15 +369,6 @@ bool plan_copy(CopyPlan &plan, Q8CopyParams &c, const Q8Params &p, int partition
     return true;
 }
 
-int check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_dim,
-                 int max_seq_len, int partition_size)
-{
-    if (num_seqs <= 0 || q_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads != 0 || head_dim <= 0 || max_seq_len < 0 || partition_size <= 0)
-        return PA_ERR_INVALID_ARG;
-    return PA_OK;
-}
-
 } // namespace
 
 extern "C" {
@@ -421,8 +412,10 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
 PA_API int pa_decode_q8_partition(int num_seqs, int q_len, int num_heads, int num_kv_heads,
                                   int head_dim, int max_seq_len, int partition_size)
 {
-    if (check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len, partition_size))
-        return -PA_ERR_INVALID_ARG;
+    const int rc = host_check_choose(num_seqs, q_len, num_heads, num_kv_heads, head_dim, max_seq_len,
+                                     partition_size);
+    if (rc)
+        return -rc;
     int dev, sms;
     if (host_device(&dev, &sms))
         return -PA_ERR_CUDA;

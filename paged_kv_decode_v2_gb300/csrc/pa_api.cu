@@ -898,6 +898,8 @@ int host_check_choose(int num_seqs, int q_len, int num_heads, int num_kv_heads, 
         return PA_ERR_INVALID_ARG;
     if (num_heads / num_kv_heads > kMaxGQA || num_seqs > 65535 || num_kv_heads > 65535)
         return PA_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return PA_ERR_UNSUPPORTED;
     return check_q_len(num_seqs, q_len);
 }
 

@@ -12,3 +12,9 @@ import pytest
 ])
 def test_sizes_that_the_calls_refuse(cuda_lib, name, seqs, q_len, heads, kv):
     assert getattr(cuda_lib.load(), name)(seqs, q_len, heads, kv, 128, 100000, 512) == -cuda_lib.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["pa_decode_q8_partition", "pa_decode_mq_partition", "pa_decode_mq_choose"])
+@pytest.mark.parametrize("head_dim", [1, 96, 192, 512])
+def test_head_dims_that_the_calls_refuse(cuda_lib, name, head_dim):
+    assert getattr(cuda_lib.load(), name)(1, 1, 8, 2, head_dim, 100000, 512) == -cuda_lib.PA_ERR_UNSUPPORTED

@@ -161,7 +161,7 @@ enum { kQ8V2, kQ8V1, kQ8If }; // kQ8If: V1 if a flag is up, any grid
 struct Q8TcKernel {
     const void *fn;
     int threads;
-    int ctas;                // per SM that its registers and tensor memory allow
+    int ctas;                // that share an SM
     size_t fixed_bytes;      // dynamic shared memory but for the rings
 };
 // rows 8, 16, 32, or (up to head_dim 128) 64; fn null otherwise.

@@ -26,8 +26,8 @@ int rows_per_cta(int cols, int head_dim)
     return cols <= 32 || head_dim == 256 ? 32 : 64;
 }
 
-// CTAs of the kernel that share an SM.
-int ctas_per_sm(int nr, int head_dim) { return nr <= 32 && head_dim <= 128 ? 2 : 1; }
+// CTAs of the kernel that share an SM, the same for both types.
+int ctas_per_sm(int nr, int head_dim) { return q8_tc(head_dim, nr, PA_F16, kQ8V2).ctas; }
 
 std::atomic<int64_t> g_tc_limit[kMaxDevices][3 * 4 * 2 * 3];
 

@@ -334,11 +334,17 @@ struct Q8Cfg {
     // TMEM columns, in regions of 32: O's halves, then the S buffers.
     static constexpr int kOReg = (kPN + 31) / 32 * 32;
     static constexpr int kSReg = (kSN + 31) / 32 * 32;
-    static constexpr int kBuf = kOReg * kMB + 2 * kSReg <= 512 ? 2 : 1; // S and P buffers
+    // CTAs that share an SM: registers (by the launch bounds), tensor memory (below) and
+    // shared memory (launch_tc's rings) are each cut to it.  32 binary16 rows: one S buffer
+    // for two CTAs, batch decode lengths 70 us, one CTA with two buffers 74 (100,000 tokens
+    // 41 and 50; 300 sequences of up to 700 41 and 52; 32 rows of one new token over 100,000
+    // 77 and 72).
+    static constexpr int kCtas = NR <= 32 && D <= 128 ? 2 : 1;
+    static constexpr int kBuf = kOReg * kMB + 2 * kSReg <= 512 / kCtas ? 2 : 1; // S and P buffers
     static constexpr int kNeed = kOReg * kMB + kBuf * kSReg;
     static constexpr uint32_t kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static constexpr uint32_t kSCol = kOReg * kMB;
-    static_assert(kNeed <= 512, "O and S exceed the tensor memory");
+    static_assert(kCtas * kCols <= 512, "the CTAs of an SM exceed its tensor memory");
     static_assert(NR * D * 4 <= 2 * kTile, "a cluster's partials lie in the smallest rings");
     static constexpr int kPW = kPN <= 32 ? 32 : kPN <= 64 ? 64 : 128; // bytes of P's rows, and
     static constexpr int kPGroups = (kPN + kPW - 1) / kPW;        // groups of that many columns
@@ -354,8 +360,6 @@ struct Q8Cfg {
     // with four; at 8 rows 100k tokens 22.0, 22.7 with two).
     static constexpr int kLoad = NR <= 8 ? 4 : 2;
     static constexpr int kThreads = kSoft + 64 + 32 * kLoad;
-    static constexpr int kMinCtas = D > 128 ? 1 : NR <= 32 ? 2 : 1;
-    static constexpr int kCtas = kMinCtas * (int)kCols <= 512 ? kMinCtas : 512 / (int)kCols;
     static constexpr uint32_t kFixed = 1024 + kBuf * kPBytes + kQBytes;
 };
 
@@ -1216,7 +1220,7 @@ __device__ __forceinline__ void q8_begin(const CUtensorMap &tmap_k, const CUtens
 // (Registers are handed out to warps by fours: launch bounds of a multiple of 128
 // threads let two CTAs share an SM.)
 template <int D, int NR, int PL, bool V1>
-__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
+__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kCtas)
     q8_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
 {
@@ -1228,7 +1232,7 @@ __global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128
 // so a CTA per SM takes all the work (two chunks of 1024 new tokens then 308 us, 314 with a
 // CTA for each unit, the wide CTAs leaving wave by wave; 31 of 390 on 3 heads 263, 282).
 template <int D, int NR, int PL>
-__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kMinCtas)
+__global__ void __launch_bounds__((Q8Cfg<D, NR, PL>::kThreads + 127) / 128 * 128, Q8Cfg<D, NR, PL>::kCtas)
     q8_tc_if_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const Q8Params p)
 {
@@ -1261,6 +1265,8 @@ static Q8TcKernel q8_tc_pick_parts(int mode)
 template <int D, int NR>
 static Q8TcKernel q8_tc_pick(int dtype, int mode)
 {
+    // (a call is cut before its type is known: pa_decode_q8_partition)
+    static_assert(Q8Cfg<D, NR, 2>::kCtas == Q8Cfg<D, NR, 3>::kCtas, "one plan for both types");
     return dtype == PA_BF16 ? q8_tc_pick_parts<D, NR, 2>(mode) : q8_tc_pick_parts<D, NR, 3>(mode);
 }
 

@@ -108,3 +108,112 @@ def test_very_negative_scores(pa, lens, P, Q, dtype):
     assert status == 0
     for b in range(len(lens)):
         assert (out[b].float() == v[tables[b, best[b] // bs], 0, best[b] % bs]).all()
+
+
+# ---------------------------------------------------------------- the parts of Q and P
+
+
+def parts_of(x, count):
+    """Rows of x as `count` e4m3 parts, part j standing for 16^-j of its value, of the row scaled to [2^7, 2^8)."""
+    x = x.double()
+    f = torch.exp2(7 - torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))))
+    rest, got = x * f, []
+    for _ in range(count):
+        p = rest.float().to(E4M3).double()
+        got.append(p)
+        rest = (rest - p) * 16
+    return sum(p / 16.0 ** j for j, p in enumerate(got)) / f
+
+
+def low_bits(D, bs, L, dtype, G, seed=3):
+    """Query rows c + d, -c on pairs of dims with equal keys: the scores are sum d k, and d lies in the bits that only the
+    last part of a query holds (fp16's low 3, bf16's low 4)."""
+    g = torch.Generator().manual_seed(seed)
+    step, high = (2.0 ** -10, 128) if dtype == F16 else (2.0 ** -7, 8)
+    top = 7 if dtype == F16 else 15
+    c = 1 + torch.randint(0, high - 1, (1, 1, G, D // 2), generator=g).double() / high
+    d = step * torch.randint(1, top + 1, (1, 1, G, D // 2), generator=g).double()
+    q = torch.stack([c + d, -c], -1).flatten(-2)
+    assert torch.equal(q.to(dtype).double(), q)
+    k = torch.randint(-15, 16, (L, D // 2), generator=g).double() / 8
+    scores = k @ d[0, 0, 0]
+    scale = 3.0 / float(scores.std())
+    v = torch.randint(-15, 16, (L, D), generator=g).float() / 8
+    n = -(-L // bs)
+    return q.to(dtype), cache_of(k.repeat_interleave(2, 1).float(), v, [1.0] * n, [1.0] * n, bs), scale
+
+
+def exact_with(q, c, scale):
+    """(out, tolerance) in 64 bits for queries q (64 bits).  Parts of a query are whole multiples of 2^-3 up to 2^8, keys of
+    2^-3 below 2: the sums over a row are multiples of 2^-6 below 2^17, exact in fp32.  A score (below 40 in log2 units)
+    is then off by some 3 roundings of 2^-24 of it and exp2 by 2^-22: together below 2^-16.  A weight is rounded to binary16
+    (2^-11 of it), and what lies below 2^-27 of the largest is lost."""
+    k, v = (x.view(torch.uint8).view(E4M3).float().double().flatten(0, 2)[:int(c[5])] for x in c[:2])
+    p = torch.softmax(q[0, 0] @ k.T * scale, 1)
+    out = p @ v
+    return out, (2.0 ** -11 + 2.0 ** -15) * (p @ v.abs()) + 2.0 ** -27 * p.amax(1, keepdim=True) * v.abs().sum(0)
+
+
+@pytest.mark.parametrize("dtype,parts", [(F16, 3), (BF16, 2)])
+def test_a_lost_part_of_q_is_seen(dtype, parts):
+    q, c, scale = low_bits(128, 16, 1000, dtype, 4)
+    ref, tol = exact_with(q.double(), c, scale)
+    tol = tol + cu.rounding(ref.abs() + tol, dtype)
+    assert torch.equal(parts_of(q, parts), q.double())
+    lost, _ = exact_with(parts_of(q, parts - 1), c, scale)
+    assert ((lost - ref).abs() > 20 * tol).double().mean() > 0.5
+
+
+@gpu
+@pytest.mark.parametrize("G", [1, 6, 12, 24, 64])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 32), (256, 8)])
+@pytest.mark.parametrize("L,P", [(100, 512), (1000, 512), (7000, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_every_part_of_q(pa, dtype, L, P, D, bs, G):
+    q, c, scale = low_bits(D, bs, L, dtype, G)
+    ref, tol = exact_with(q.double(), c, scale)
+    out, status = run(pa, q, c, scale, P)
+    assert status == 0
+    assert ((out[0, 0].double() - ref).abs() <= tol + cu.rounding(ref.abs() + tol, dtype)).all()
+
+
+def even_weights(D, bs, L, dtype):
+    """Weights of 2047/2048 of the largest (eleven ones: every part of P is needed, and what is lost of it adds up), in all
+    blocks but the first of every 128 tokens, whose weight is 1.  V is one value, just above the middle between two values of the
+    output's type: the exact result is that value, and one that is smaller by 2^-11 rounds down."""
+    n = -(-L // bs)
+    x = -math.log(2047 / 2048)
+    k = torch.zeros(L, D)
+    k[:, 0] = -1.0
+    k[(torch.arange(L) % 128) < bs] = 0.0
+    middle = 1 + cu.HALF_STEP[dtype]
+    value = float(torch.tensor(middle * (1 + 2.0 ** -12)).float())
+    return cache_of(k, torch.ones(L, D), [x] * n, [value] * n, bs), value
+
+
+def rounded_up(dtype):
+    return 1 + 2 * cu.HALF_STEP[dtype]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bs", [8, 64])
+def test_a_lost_part_of_p_is_seen(dtype, bs):
+    c, value = even_weights(64, bs, 1280, dtype)
+    w = torch.where((torch.arange(1280) % 128) < bs, 2048.0, 2047.0).double()
+    lost = torch.where(w == 2047, 2044.0, w)  # without the fourth part: 3 + 3 + 3 bits
+    assert float((torch.tensor(value).double() * lost.sum() / w.sum()).to(dtype)) < rounded_up(dtype)
+    assert float(torch.tensor(value).to(dtype)) == rounded_up(dtype)
+
+
+@gpu
+@pytest.mark.parametrize("G", [1, 6, 12, 24, 64])
+@pytest.mark.parametrize("D,bs", [(64, 64), (128, 32), (256, 8)])
+@pytest.mark.parametrize("L,P", [(100, 512), (1000, 512), (7000, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_every_part_of_p(pa, dtype, L, P, D, bs, G):
+    """(exp2, the sums and the quotient are off by less than 2^-19: no weight's rounding moves, and the result rounds up.)"""
+    c, value = even_weights(D, bs, L, dtype)
+    q = torch.zeros((1, 1, G, D), dtype=dtype)
+    q[..., 0] = 1.0
+    out, status = run(pa, q, c, 1.0, P)
+    assert status == 0 and (out.float() == rounded_up(dtype)).all()

@@ -44,6 +44,11 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _text(path: str) -> str:
+    with open(path) as f:
+        return f.read()
+
+
 def _run(cmd, what: str):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -104,8 +109,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if force or _stale(BIND, [bind_obj]):
+    # Which torch's object _bind.so holds: another torch's may be older than the link.
+    linked, name = os.path.join(BUILD, "bind-linked"), os.path.basename(bind_obj)
+    if force or _stale(BIND, [bind_obj]) or not os.path.exists(linked) or _text(linked) != name:
         _link_bind(bind_obj)
+        with open(linked, "w") as f:
+            f.write(name)
     return LIB
 
 

@@ -71,9 +71,8 @@ __global__ void __launch_bounds__(NTH) merge_kernel(const MergeParams p)
     if (np == 0) {
         if (threadIdx.x < DD)
             out[threadIdx.x] = E::from_float(0.f);
-        return;
     }
-    if (p.single_done && np == 1) {
+    if (np == 0 || (p.single_done && np == 1)) {
         asm volatile("griddepcontrol.wait;" ::: "memory"); // this grid ends after phase 1
         return;
     }
@@ -168,9 +167,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergePa
 #pragma unroll
         for (int j = 0; j < DL; ++j)
             out[j] = E::from_float(0.f);
-        return;
     }
-    if (p.single_done && np == 1) {
+    if (np == 0 || (p.single_done && np == 1)) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }

@@ -27,10 +27,13 @@
 // rounding of 16 times what x_(k-1) left: two parts hold bf16's 8 significant
 // bits, three binary16's 11, exactly down to 2^-6 of that scale (and to 2^-14,
 // 2^-18 absolute below); the parts' products meet in fp32.  A weight is rounded
-// to binary16 (2^-12 of itself) and then split without error: e5m2 is binary16's
-// upper byte, so each of the four parts is the upper byte of what the parts
-// before it left (3 + 3 + 3 + 2 bits).  Weights of 1 are stored as 2^11, so that
-// what falls below e5m2's smallest step, 2^-16, is below 2^-27 of them.
+// to binary16 (2^-11 of itself) and then split without error, w = w_0 + w_1 / 8 +
+// w_2 / 64 + w_3 / 512: e5m2 is binary16's upper byte, so each of the four parts is
+// the upper byte of 8 times what the part before it left (3 + 3 + 3 + 2 bits; what a
+// part leaves is below a quarter of its power of two, so that 8 times it stays within
+// the weights' bound of 2^15, and e5m2's smallest step, 2^-16, is 2^-25 of w_3).  Weights
+// of 1 are stored as 2^11: those below 2^-25 of them are binary16's subnormals, off by at
+// most 2^-36.
 //
 // V's scales go into the softmax's exponent.  With r the largest V scale of the
 // CTA's range and lv_t = log2(vs_t / r), floored at -60,
@@ -95,6 +98,13 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b)
 {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t h2_times8(uint32_t a)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x48004800u));
     return r;
 }
 
@@ -1042,8 +1052,8 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
                 for (int k = 0; k < 4; ++k) {
                     w[k][r / 4] = __byte_perm(h[0], h[1], 0x7531); // upper bytes
                     if (k < 3) {
-                        h[0] = h2_sub(h[0], h[0] & 0xff00ff00u);
-                        h[1] = h2_sub(h[1], h[1] & 0xff00ff00u);
+                        h[0] = h2_times8(h2_sub(h[0], h[0] & 0xff00ff00u));
+                        h[1] = h2_times8(h2_sub(h[1], h[1] & 0xff00ff00u));
                     }
                 }
             }
@@ -1141,7 +1151,7 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
             *abort_flag = 1;
         }
 
-        // ---- epilogue: thread = dim, O of its rows from the three parts
+        // ---- epilogue: thread = dim, O of its rows from the four parts
         if (ok && tk < D) {
 #pragma unroll 1
             for (int h = 0; h < C::kMB; ++h) {
@@ -1159,9 +1169,11 @@ __device__ __forceinline__ bool q8_unit(const CUtensorMap &tmap_k, const CUtenso
                     for (int i = 0; i < 8; ++i) {
                         const int r = row0 + r8 + i;
                         if (r < nrows) {
-                            const float v = ((__uint_as_float(o[3][i]) + __uint_as_float(o[2][i])) +
-                                             (__uint_as_float(o[1][i]) + __uint_as_float(o[0][i]))) *
-                                            s_inv[r];
+                            float v = __uint_as_float(o[3][i]);
+#pragma unroll
+                            for (int k = 2; k >= 0; --k)
+                                v = fmaf(v, 0.125f, __uint_as_float(o[k][i]));
+                            v *= s_inv[r];
                             if (V1 && ways > 1) // every tile of the rings is read by now
                                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem0 + (r * D + d) * 4), "f"(v)
                                              : "memory");

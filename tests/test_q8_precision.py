@@ -217,3 +217,52 @@ def test_every_part_of_p(pa, dtype, L, P, D, bs, G):
     q[..., 0] = 1.0
     out, status = run(pa, q, c, 1.0, P)
     assert status == 0 and (out.float() == rounded_up(dtype)).all()
+
+
+# ---------------------------------------------------------------- small weights beside a large one
+
+
+def sink(D, bs, L, exponent):
+    """One token of weight 1 whose V is 0, and L - 1 of weight 2047 * 2^exponent (eleven ones) whose V is 1: the result is
+    what the small ones add up to."""
+    n = -(-L // bs)
+    w = 2047 * 2.0 ** exponent
+    k = torch.zeros(L, D)
+    k[1:, 0] = -1.0
+    v = torch.ones(L, D)
+    v[0] = 0.0
+    return cache_of(k, v, [-math.log(w)] * n, [1.0] * n, bs), (L - 1) * w / (1 + (L - 1) * w)
+
+
+def sink_tolerance(ref, L, dtype):
+    """A weight, in units of 2^-11, is rounded to binary16: by 2^-11 of it, or 2^-25 where that is more; exp2 and the sums
+    add less than 2^-18."""
+    tol = ref * (2.0 ** -11 + 2.0 ** -18) + L * 2.0 ** -36
+    return tol + float(cu.rounding(torch.tensor(ref + tol, dtype=torch.float64), dtype))
+
+
+@pytest.mark.parametrize("exponent", [-31, -34])
+def test_truncated_small_weights_are_seen(exponent):
+    """Parts that end at 2^-16 of those units (e5m2's smallest step, without a factor between them)."""
+    ref = sink(64, 16, 8000, exponent)[1]
+    w = 2047 * 2.0 ** (exponent + 11)
+    kept = math.floor(w * 2 ** 16) / 2 ** 16
+    assert ref * (1 - kept / w) > sink_tolerance(ref, 8000, F16)
+
+
+@gpu
+@pytest.mark.parametrize("exponent", [-31, -34, -37])
+@pytest.mark.parametrize("G", [4, 16, 30, 60])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 32), (256, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_small_weights_beside_a_large_one(pa, dtype, D, bs, G, exponent):
+    """All tokens of a sequence in one CTA."""
+    S, L = 200, 8000
+    c, ref = sink(D, bs, L, exponent)
+    c = c[:4] + (c[4].expand(S, -1).contiguous(), c[5].expand(S).contiguous())
+    q = torch.zeros((S, 1, G, D), dtype=dtype)
+    q[..., 0] = 1.0
+    out, status = run(pa, q, c, 1.0, 8192)
+    tol = sink_tolerance(ref, L, dtype)
+    assert status == 0
+    assert ((out.double() - ref).abs() <= tol).all(), (float((out.double() - ref).abs().max()), ref, tol)

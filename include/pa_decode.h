@@ -524,7 +524,7 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  * blocks, beside the partials) and runs pa_decode_mq's kernels over that.
  * The copy holds what it stands for exactly, under scales that are powers of
  * two, as pa_kv_append_q8 writes them, in the type's range (binary16 [2^-15,
- * 2^7], bfloat16 [2^-117, 2^119], or 0).  A nonzero code under any other scale
+ * 2^7], bfloat16 [2^-60, 2^60], or 0).  A nonzero code under any other scale
  * is found on the device, and the 8-bit kernel runs instead.
  *
  * V scales are not negative: one that is, or that is not finite, makes NaN of

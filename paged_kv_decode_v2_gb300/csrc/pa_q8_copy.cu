@@ -73,13 +73,14 @@ __global__ void __launch_bounds__(kScanThreads) q8_offsets_kernel(const Q8CopyPa
 }
 
 // Whether T holds every code times s: e4m3 has 4 significant bits and values from 2^-9 to
-// 448 = 1.75 * 2^8.  binary16 holds multiples of 2^-24 and up to 65504; bf16's range is
-// kept to its normal values, from 2^-126.
+// 448 = 1.75 * 2^8.  binary16 holds multiples of 2^-24 and up to 65504.  bf16 would hold
+// them from 2^-117 to 2^119, but there a sum of products with a query can leave fp32's
+// range where the 8-bit kernel's, of codes, does not: far within it, 2^-60 to 2^60.
 template <typename T>
 __device__ __forceinline__ bool exact_under(float s)
 {
-    const float lo = Elem<T>::kSplitP ? 6.018531076210112e-36f : 3.0517578125e-5f; // 2^-117, 2^-15
-    const float hi = Elem<T>::kSplitP ? 6.646139978924579e35f : 128.f;             // 2^119, 2^7
+    const float lo = Elem<T>::kSplitP ? 8.673617379884035e-19f : 3.0517578125e-5f; // 2^-60, 2^-15
+    const float hi = Elem<T>::kSplitP ? 1.152921504606847e18f : 128.f;             // 2^60, 2^7
     return s == 0.f || ((__float_as_uint(s) & 0x7fffffu) == 0u && s >= lo && s <= hi);
 }
 

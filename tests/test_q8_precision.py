@@ -81,6 +81,27 @@ def test_scales_are_kept_whatever_the_rows_and_the_workspace(pa, D, dtype, Q, G)
         assert ((out - ref).abs() <= tol + cu.rounding(ref.abs() + tol, dtype)).all(), float((out - ref).abs().max())
 
 
+@gpu
+@pytest.mark.parametrize("up", [105, -100])
+@pytest.mark.parametrize("Q", [70, 900])
+@pytest.mark.parametrize("D", [64, 256])
+def test_extreme_scales_are_kept_whatever_the_rows(pa, D, Q, up):
+    """bf16 queries and K scales whose sums of products leave fp32's range, and a softmax scale that brings the scores back
+    to a size of 4: the 8-bit kernel's sums are of codes, those over a 16-bit copy would be infinite."""
+    c = list(cu.cache8([4800], KV=1, D=D, bs=16, seed=up))
+    c[2] = c[2] * 2.0 ** up
+    g = torch.Generator().manual_seed(9)
+    few = 125 - up if up > 0 else -140 - up
+    q = (torch.randn((1, Q, 4, D), generator=g) * 2.0 ** few).to(BF16)
+    scale = 2.0 ** -126 if up > 0 else 2.0 ** 127
+    ref, tol = cu.attend_reference(q[:, -2:], *c, scale)
+    assert torch.isfinite(ref).all()
+    out, status = run(pa, q, c, scale, 128)
+    out = out[:, -2:].double()
+    assert status == 0
+    assert ((out - ref).abs() <= tol + cu.rounding(ref.abs() + tol, BF16)).all(), float((out - ref).abs().max())
+
+
 # ---------------------------------------------------------------- scores of any finite size
 
 

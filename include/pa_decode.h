@@ -437,8 +437,8 @@ PA_API int pa_set_merge_form(int form);
  * token_starts (device, [num_seqs + 1] int32, not decreasing) sequence b's
  * new tokens are the rows token_starts[b] <= t < token_starts[b + 1], none
  * when the two are equal; rows before token_starts[0] or from
- * token_starts[num_seqs] on belong to no sequence and are neither read nor
- * written anywhere.  With token_starts NULL every sequence has num_tokens /
+ * token_starts[num_seqs] on belong to no sequence: nothing is written for
+ * them, nor to their rows of query_out, whatever they hold.  With token_starts NULL every sequence has num_tokens /
  * num_seqs of them (num_tokens must be a multiple of num_seqs): row b * q_len
  * + i.  seq_lens[b] counts the new tokens, as pa_decode expects it
  * afterwards: the last of them sits at position seq_lens[b] - 1.  A token at
@@ -519,9 +519,15 @@ PA_API int pa_kv_append_q8(const void *key, const void *value, int64_t key_strid
  * their contents after the call are unspecified.
  *
  * From 256 query rows (q_len * G) per KV head and 2048 tiles (of 128 tokens up
- * to max_seq_len by 64 rows) on, when tmp_output has room for it, the call first makes a 16-bit copy of the blocks that it reads there (in
- * the query's type, K and V of num_seqs * ceil(max_seq_len / block_size)
- * blocks, beside the partials) and runs pa_decode_mq's kernels over that.
+ * to max_seq_len by 64 rows) on, when tmp_output has room for it, the call
+ * first makes a 16-bit copy of the blocks that it reads there (in the query's
+ * type, K and V of num_seqs * ceil(max_seq_len / block_size) blocks, beside
+ * the partials that pa_decode_mq would write) and runs pa_decode_mq's kernels
+ * over that, up to twice as fast and with their rounding of the softmax's
+ * weights.  The room is there when max_num_partitions counts partitions of at
+ * most about q_len * G tokens: intermediates sized for partition_size hold
+ * the copy from about partition_size rows on, and a larger max_num_partitions
+ * makes room for fewer.
  * The copy holds what it stands for exactly, under scales that are powers of
  * two, as pa_kv_append_q8 writes them, in the type's range (binary16 [2^-15,
  * 2^7], bfloat16 [2^-60, 2^60], or 0).  A nonzero code under any other scale

@@ -10,9 +10,12 @@
 // storage type (or straight to 8 bits).
 //
 // Measured on a GB300 (us a call, share of the measured copy bandwidth): 64 prompts
-// of up to 2048 tokens, 64 heads on 8, 128 dims: 410 (98%), to 8 bits 404 (94%);
-// two chunks of 2048 tokens, 32 heads on 8, to 8 bits: 18.5 (75%); 32 single tokens
-// to 8 bits 3.2, one token 2.6 (latency and launch).
+// of up to 2048 tokens, 64 heads on 8, 128 dims, blocks of 32: 410 (98%), to 8 bits 404
+// (94%; blocks of 8 405, of 64 460, 83%); 32 such prompts of 256 dims 399 (100%), to 8
+// bits 446 (85%) at blocks of 32 and 468 (81%) of 64, whose wide CTAs of several heads
+// spill; 64 of 64 dims 242 (83%), to 8 bits 244 (78%).  Two chunks of 2048 tokens, 32
+// heads on 8, to 8 bits: 18.7 (74%); 32 single tokens to 8 bits 3.4, one token 2.7
+// (latency and launch).
 //
 // 16-bit caches: a pure copy with three operations per value, bound by bytes
 // on prompts and by its chain of dependent loads (starts -> length -> block

@@ -304,9 +304,12 @@ Q8Cut choose_cut(int num_seqs, int q_len, int group, int num_kv_heads, int head_
 // ---- the 16-bit copy for many rows
 
 // From this many query rows per KV head on, the call makes a 16-bit copy of its
-// blocks and runs the 16-bit kernels over it.  8 KV heads, copy / 8-bit kernel, us: 2
-// sequences of 9000 tokens 128 rows 56 / 52, 256 rows 67 / 82, 1024 rows 116 / 259;
-// 16 of 2000 86 / 75, 99 / 146, 247 / 489.
+// blocks and runs the 16-bit kernels over it, if the intermediates have room (plan_copy;
+// sized for partition_size, from about that many rows on) and its scales let the copy be
+// exact.  8 KV heads, copy / 8-bit kernel, us: 2 sequences of 9000 tokens 128 rows 56 / 52,
+// 256 rows 67 / 82, 1024 rows 116 / 259; 16 of 2000 86 / 76, 99 / 146, 238 / 489.  Where a
+// scale is no power of two both run, the copy's attention for nothing but its launch: 2
+// sequences of 9216 tokens, 4096 rows 328 -> 829 (fp16 319 -> 1119).
 constexpr int kQ8CopyRows = 256;
 // And from this many tiles of 128 tokens by 64 rows on: one sequence of 4000 tokens, 256
 // rows (992 tiles) 32 / 27, 512 rows (1984) 42 / 40, 2048 rows (7936) 60 / 114; 20,000

@@ -55,11 +55,12 @@
 // take units of work in order of size.
 //
 // Measured on a GB300 (us a call, and its bytes as a share of the measured copy
-// bandwidth): 32 sequences of up to 8192 tokens, 32 heads on 8: 52 (80%); one of
-// 100,000 tokens on 4 KV heads: 21.7 (70%); 64 of up to 32,768, 64 heads on 8: 73
-// (100%); 8 of 131,072: 323 (98%); one of 1000: 7.0, latency.  16 new tokens for 32
-// sequences: 89 (46%), bound by the softmax warps: some 400 instructions a warp and
-// tile, about 140 of them arithmetic, more than half of that the parts of P and Q.
+// bandwidth): 32 sequences of up to 8192 tokens, 32 heads on 8: 45-49 (82%); one of
+// 100,000 tokens on 4 KV heads: 22.6 (67%); 64 of up to 32,768, 64 heads on 8: 71-80
+// (its own 497 MB in 73: 100%); 8 of 131,072: 321-324 (98%); one of 1000: 6.7, latency.
+// 16 new tokens for 32 sequences: 83-86 (48%), bound by the softmax warps: some 400
+// instructions a warp and tile, about 160 of them arithmetic, more than half of that the
+// parts of P and Q (the factors between P's parts 2-3% of the time).
 //
 // Built and measured slower: the same work on mma.sync (16 new tokens 278); equal
 // stretches of tiles over a fixed grid (16 new tokens 166 where partitions took

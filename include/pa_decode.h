@@ -438,9 +438,10 @@ PA_API int pa_set_merge_form(int form);
  * new tokens are the rows token_starts[b] <= t < token_starts[b + 1], none
  * when the two are equal; rows before token_starts[0] or from
  * token_starts[num_seqs] on belong to no sequence: nothing is written for
- * them, nor to their rows of query_out, whatever they hold.  With token_starts NULL every sequence has num_tokens /
- * num_seqs of them (num_tokens must be a multiple of num_seqs): row b * q_len
- * + i.  seq_lens[b] counts the new tokens, as pa_decode expects it
+ * them, nor to their rows of query_out, whatever they hold.  With
+ * token_starts NULL every sequence has num_tokens / num_seqs of them
+ * (num_tokens must be a multiple of num_seqs): row b * q_len + i.
+ * seq_lens[b] counts the new tokens, as pa_decode expects it
  * afterwards: the last of them sits at position seq_lens[b] - 1.  A token at
  * position n goes to row n % block_size of block block_tables[b][n /
  * block_size].

@@ -699,9 +699,12 @@ PA_API int pa_decode_q4_partition(int num_seqs, int q_len, int num_heads, int nu
  * groups of a 4-bit K whose scale is below 2^-27 of the largest among 128 tokens
  * side by side may count as 0.  A score that is not finite makes NaN of its row's
  * weights.  max_blocks_per_seq * block_size is at
- * most 2^31 - 65537.  Sequences that share blocks: a shared token's slot gets
- * either's weights.  Device-side problems as pa_decode's; a token in a block
- * outside the pool gets no weight.
+ * most 2^31 - 65537.  Sequences may share blocks: slots behind a sequence's
+ * last token are left to the others.  A token that several sequences of a call
+ * hold has one slot, which afterwards has one of their updates, or several one
+ * after the other (each with its decay and its sum), whichever came when.
+ * Device-side problems as pa_decode's; a token in a block outside the pool gets
+ * no weight.
  */
 PA_API int pa_kv_weights(const void *query, const void *key_cache, const int32_t *block_tables,
                          const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,

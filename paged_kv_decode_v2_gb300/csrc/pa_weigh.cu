@@ -447,17 +447,23 @@ __global__ void __launch_bounds__(kSumThreads, V * kAhead <= 16 ? 6 : 4) weights
     }
     if (!at)
         return;
-    // The newest tokens have no weight of earlier calls, whatever their slots hold; slots
-    // behind the last token keep what they hold.
+    // The newest tokens have no weight of earlier calls, whatever their slots hold.
 #pragma unroll
     for (int k = 0; k < V; ++k)
-        now[k] = t + k >= L           ? now[k]
-                 : t + k < L - p.q_len ? fmaf(now[k], p.decay, sum[k])
-                                       : sum[k];
-    if constexpr (V == 4)
-        *reinterpret_cast<float4 *>(at) = make_float4(now[0], now[1], now[2], now[3]);
-    else
-        *reinterpret_cast<float2 *>(at) = make_float2(now[0], now[1]);
+        now[k] = t + k < L - p.q_len ? fmaf(now[k], p.decay, sum[k]) : sum[k];
+    // Slots behind the last token may be another sequence's, whose update would be lost under
+    // one of this thread's: they are not written.
+    if (t + V <= L) {
+        if constexpr (V == 4)
+            *reinterpret_cast<float4 *>(at) = make_float4(now[0], now[1], now[2], now[3]);
+        else
+            *reinterpret_cast<float2 *>(at) = make_float2(now[0], now[1]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (t + k < L)
+                at[k] = now[k];
+    }
 }
 
 std::atomic<int> g_prepared[64][3 * 3 * 4]; // [type, head_dim, rows]

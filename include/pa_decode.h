@@ -685,7 +685,7 @@ PA_API int pa_decode_q4_partition(int num_seqs, int q_len, int num_heads, int nu
  * without the first term for the q_len newest tokens (t >= seq_lens[b] -
  * q_len), whose slots' contents are not read.  decay 1 adds up over all calls,
  * 0 keeps the last call's alone (a window of queries at a prompt's end, or the
- * newest query).
+ * newest query) and reads no slot, so that what they hold does not matter.
  *   weights    [num_blocks, num_kv_heads, block_size] float32, 16-byte aligned:
  *              a token's lies where its key does.  Sums over rows are fp32, in
  *              a fixed order.

@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kSumThreads, V * kAhead <= 16 ? 6 : 4) weights
     float now[V] = {};
     if (t < L) {
         at = weight_at(p, b, kv, t);
-        if (at)
+        if (at && p.decay != 0.f) // (0 times what is not finite would be NaN)
             load_v(at, now);
     }
     const int parts = (int)(((unsigned)L + p.part - 1) / p.part);

@@ -530,7 +530,9 @@ __global__ void __launch_bounds__((kThreads + 127) / 128 * 128, D <= 128 ? 2 : 1
                     float old = 0.f;
                     if (rt + 1 == rt1 && pos < tokE) {
                         slot = weight_at(p, b, kv, pos);
-                        if (slot && pos < rel) // (the newest tokens have none, whatever their slots hold)
+                        // (The newest tokens have none, whatever their slots hold; 0 times what is not
+                        // finite would be NaN.)
+                        if (slot && pos < rel && p.decay != 0.f)
                             old = *slot;
                     }
                     if (!__all_sync(0xffffffffu, mbar_wait_abortable(b_s_full + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag))) {

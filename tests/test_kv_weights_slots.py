@@ -43,3 +43,41 @@ def test_a_longer_sequence_in_a_shared_block(pa, short, long, Q, G, bits):  # no
             for at in range(long):
                 rest[tables[i, at // bs], :, at % bs] = False
         assert torch.equal(got[rest], w[rest])
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("Q,G,D", [(1, 1, 64), (1, 4, 128), (5, 8, 64), (3, 16, 256), (16, 2, 128), (20, 4, 64), (40, 8, 256)])
+@pytest.mark.parametrize("held", [math.nan, math.inf, -math.inf])
+def test_decay_zero_reads_nothing(pa, held, Q, G, D, bits):  # noqa: F811
+    """decay 0 keeps the call's own sums alone, whatever the slots hold."""
+    lens = [0, 1, 7, 64, 65, 1300]
+    q, kc, ks, tables, n, w = inputs(lens, Q, G, 2, D, 16, F16, bits, Q)
+    ref, tol = q4.weigh_reference(q, kc, ks, tables, n, 0.1, torch.zeros_like(w), 0.0)
+    got, status = run(pa, q, kc, ks, tables, n, torch.full_like(w, held), 0.1, 0.0)
+    assert status == 0
+    for b, L in enumerate(lens):
+        x, r, t = (slots(y, tables, b, L) for y in (got.double(), ref, tol))
+        assert ((x - r).abs() <= t).all(), (L, x, r)
+    # With any other decay what they hold counts.
+    got, status = run(pa, q, kc, ks, tables, n, torch.full_like(w, held), 0.1, 0.5)
+    assert status == 0 and not torch.isfinite(slots(got, tables, 5, 1300 - Q)).any()
+
+
+def test_a_prompt_longer_than_its_window(pa):  # noqa: F811
+    """Into weights that nobody has initialised: a prompt whose last 20 tokens are counted with decay 0, then single
+    tokens added up, are the sums from the definition."""
+    L, Q, steps, D, bs, KV, G = 200, 20, 6, 64, 16, 2, 3
+    q, kc, ks, tables, _, w = inputs([L + steps], Q + steps, G, KV, D, bs, F16, 4, 2)
+    kc, ks, tables = kc.cuda(), ks.cuda(), tables.cuda()
+    dev = torch.full(w.shape, math.nan, device="cuda")
+    ws = pa.alloc_weights_workspace(1, G * KV, tables.shape[1] * bs, q_len=Q)
+    calls = [(q[:, :Q], L, 0.0)] + [(q[:, Q + i], L + i + 1, 1.0) for i in range(steps)]
+    ref, off = torch.zeros(w.shape, dtype=torch.float64), torch.zeros(w.shape, dtype=torch.float64)
+    for x, length, decay in calls:
+        n = torch.tensor([length], dtype=torch.int32)
+        pa.pa_kv_weights(x.contiguous().cuda(), kc, tables, n.cuda(), 0.125, dev, ws, k_scales=ks, decay=decay)
+        got, t = q4.weigh_reference(x if x.dim() == 4 else x[:, None], kc.cpu(), ks.cpu(), tables.cpu(), n, 0.125,
+                                    torch.zeros(w.shape), 0.0)
+        ref, off = ref + got, off + t
+    x, r, t = (slots(y, tables.cpu(), 0, L + steps) for y in (dev.cpu().double(), ref, off))
+    assert ((x - r).abs() <= t + steps * 2.0 ** -23 * r).all()

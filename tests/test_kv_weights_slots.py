@@ -81,3 +81,19 @@ def test_a_prompt_longer_than_its_window(pa):  # noqa: F811
         ref, off = ref + got, off + t
     x, r, t = (slots(y, tables.cpu(), 0, L + steps) for y in (dev.cpu().double(), ref, off))
     assert ((x - r).abs() <= t + steps * 2.0 ** -23 * r).all()
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("Q,G", [(2, 4), (5, 1), (7, 8), (15, 3), (16, 3), (20, 4)])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_tokens_hidden_from_a_row_that_is_not_finite(pa, bad, Q, G, bits):  # noqa: F811
+    """A row whose scores are not finite makes NaN of the weights of the tokens that it sees, not of later ones."""
+    L = 50
+    q, kc, ks, tables, n, w = inputs([L, 33], Q, G, 2, 64, 16, F16, bits, Q)
+    at = Q // 2 - 1
+    q[0, at, G, 9] = bad  # new token `at`, KV head 1: sees L - Q + at + 1 tokens
+    got, status = run(pa, q, kc, ks, tables, n, w, 0.1, 1.0)
+    of = slots(got, tables, 0, L)
+    sees = L - Q + at + 1
+    assert status == 0 and torch.isnan(of[1, :sees]).all() and torch.isfinite(of[1, sees:]).all()
+    assert torch.isfinite(of[0]).all() and torch.isfinite(slots(got, tables, 1, 33)).all()

@@ -697,14 +697,14 @@ PA_API int pa_decode_q4_partition(int num_seqs, int q_len, int num_heads, int nu
  * scales; a cache in 8 bits is not supported (its scales belong to blocks, so
  * that pa_kv_evict could not move its tokens one by one).  From 16 new tokens on
  * groups of a 4-bit K whose scale is below 2^-27 of the largest among 128 tokens
- * side by side may count as 0.  A score that is not finite makes NaN of its row's
- * weights.  max_blocks_per_seq * block_size is at
- * most 2^31 - 65537.  Sequences may share blocks: slots behind a sequence's
- * last token are left to the others.  A token that several sequences of a call
- * hold has one slot, which afterwards has one of their updates, or several one
- * after the other (each with its decay and its sum), whichever came when.
- * Device-side problems as pa_decode's; a token in a block outside the pool gets
- * no weight.
+ * side by side may count as 0.  A score of +infinity or NaN makes NaN of its
+ * row's weights of the tokens that the row sees; one of -infinity is a weight of
+ * 0.  max_blocks_per_seq * block_size is at most 2^31 - 65537.  Sequences may
+ * share blocks: slots behind a sequence's last token are left to the others.  A
+ * token that several sequences of a call hold has one slot, which afterwards has
+ * one of their updates, or several one after the other (each with its decay and
+ * its sum), whichever came when.  Device-side problems as pa_decode's; a token in
+ * a block outside the pool gets no weight.
  */
 PA_API int pa_kv_weights(const void *query, const void *key_cache, const int32_t *block_tables,
                          const int32_t *seq_lens, int num_seqs, int q_len, int num_heads,

@@ -367,9 +367,11 @@ __global__ void __launch_bounds__((kThreads + 127) / 128 * 128, D <= 128 ? 2 : 1
             if (rt > rt0) // the rows before this one's have been used
                 asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
             // Q rows into shared memory: as they are beside 16-bit keys; beside codes in
-            // binary16 scaled to [2^14, 2^15).
+            // binary16 scaled to [2^14, 2^15).  Padding rows are the last row again: weight 0,
+            // as their M is infinite, while zeros would make NaN of an infinite key.  (Padding
+            // follows the last new token alone, which sees every key.)
             auto row_of = [&](int at) -> const uint8_t * {
-                const int x = c0 + (at < nrows ? at : 0), t = new_token(x);
+                const int x = c0 + min(at, nrows - 1), t = new_token(x);
                 return static_cast<const uint8_t *>(p.query) +
                        ((size_t)(b * p.q_len + t) * p.num_heads + (kv * p.group + x - t * p.group)) * (D * 2);
             };
@@ -382,12 +384,11 @@ __global__ void __launch_bounds__((kThreads + 127) / 128 * 128, D <= 128 ? 2 : 1
                     const uint8_t *const from = row_of(at) + piece * 16;
                     const uint32_t to = q_sm + (piece >> 3) * kSlice + at * 128 + (((piece & 7) ^ (at & 7)) << 4);
                     if (aligned) {
-                        q4_copy16(to, from, at < nrows ? 16u : 0u);
+                        q4_copy16(to, from, 16u);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * k),
-                                         "l"(from + 4 * k), "r"(at < nrows ? 4u : 0u)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * k), "l"(from + 4 * k)
                                          : "memory");
                     }
                 }

@@ -97,3 +97,20 @@ def test_tokens_hidden_from_a_row_that_is_not_finite(pa, bad, Q, G, bits):  # no
     sees = L - Q + at + 1
     assert status == 0 and torch.isnan(of[1, :sees]).all() and torch.isfinite(of[1, sees:]).all()
     assert torch.isfinite(of[0]).all() and torch.isfinite(slots(got, tables, 1, 33)).all()
+
+
+@pytest.mark.parametrize("Q,G", [(1, 4), (6, 8), (20, 4)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_a_score_of_minus_infinity_counts_as_nothing(pa, dtype, Q, G):  # noqa: F811
+    """16-bit keys with an infinite value, every score of which is -inf: softmax weight 0, the others' sums as ever."""
+    L = 100
+    q, kc, ks, tables, n, w = inputs([L, 20], Q, G, 2, 64, 16, dtype, 16, 4)
+    q[..., 3] = -q[..., 3].abs() - 1
+    for t in (0, 17, 70):
+        kc[tables[0, t // 16], :, t % 16, 3] = math.inf
+    got, status = run(pa, q, kc, ks, tables, n, w, 0.1, 1.0)
+    far, gone = (torch.where(torch.isinf(kc), torch.full_like(kc, x), kc) for x in (2.0 ** 14, 0.0))
+    ref, _ = q4.weigh_reference(q, far, ks, tables, n, 0.1, w, 1.0)   # weight e^-1638 and less: 0 in 64 bits too
+    _, tol = q4.weigh_reference(q, gone, ks, tables, n, 0.1, w, 1.0)  # (a far key's size is no error of the others')
+    x, r, t = (slots(y, tables, 0, L) for y in (got.double(), ref, tol))
+    assert status == 0 and ((x - r).abs() <= t).all()

@@ -641,7 +641,8 @@ PA_API int pa_kv_gather_q4(const void *key_cache, const void *value_cache, const
  * intermediates hold afterwards.  max_blocks_per_seq * block_size is at most
  * 2^31 - 65537.
  *
- * Softmax weights below 2^-25 of a row's largest may count as 0, and so may
+ * Softmax weights are rounded to binary16 once, by 2^-11 of themselves at most;
+ * those below 2^-25 of a row's largest may count as 0, and so may
  * groups of V whose scale is below 2^-26 of the largest that the call reads for
  * the same sequence and KV head and, from 33 query rows per KV head (q_len * G)
  * on, groups of K whose scale is below 2^-27 of the largest among 64 tokens side
@@ -686,6 +687,11 @@ PA_API int pa_decode_q4_partition(int num_seqs, int q_len, int num_heads, int nu
  * q_len), whose slots' contents are not read.  decay 1 adds up over all calls,
  * 0 keeps the last call's alone (a window of queries at a prompt's end, or the
  * newest query) and reads no slot, so that what they hold does not matter.
+ * Otherwise the slots of older tokens count whatever they hold.  A token that no
+ * call has had among its q_len newest (of a prompt longer than its window, or
+ * appended between two calls that ask for the newest query alone) has a slot
+ * that may hold an evicted token's weight, or nothing written yet: it is the
+ * caller's to set to 0, if the first call that counts it has another decay.
  *   weights    [num_blocks, num_kv_heads, block_size] float32, 16-byte aligned:
  *              a token's lies where its key does.  Sums over rows are fp32, in
  *              a fixed order.
@@ -739,7 +745,8 @@ PA_API size_t pa_kv_weights_workspace_bytes(int num_seqs, int q_len, int num_hea
  *              or a table whose blocks are none of those that the call reads
  *              (which other sequences may share): all that stays is copied
  *              there.  dst_max_blocks * block_size is at least the smaller of
- *              budget and the longest length.
+ *              budget and L, L = max_seq_len_hint if > 0, else
+ *              max_blocks_per_seq * block_size.
  *   kept       [num_seqs, num_kv_heads, budget] int32, written: the position
  *              that place j's token had, for j < new_lens[b]; the rest is left
  *   new_lens   [num_seqs] int32, written: min(seq_lens[b], budget); may be

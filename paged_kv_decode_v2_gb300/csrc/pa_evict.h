@@ -49,7 +49,7 @@ struct WeighParams {
     float *weights;              // [num_blocks, KV, block_size]
     int32_t *status;
 };
-// rows per CTA: 8, 16, 32 or 64; CTAs that share an SM, and their threads.
+// rows per CTA: 8, 16, 32 or 64; CTAs that registers let share an SM, and their threads.
 int weigh_ctas(int rows);
 int weigh_threads();
 cudaError_t launch_weigh(int head_dim, int rows, const WeighParams &p, int dev, cudaStream_t stream);

@@ -7,20 +7,28 @@
 // tokens (this file): the first writes the scores (fp32, in log2 units) beside each
 // partition's maximum and sum, and the second turns them into weights and sums them over
 // the rows; the keys are read once, and scores of a decode step, rows * 4 bytes a token
-// and head beside 68 (4-bit) to 512 bytes of keys, mostly stay in L2.  From kWeighAgain
-// new tokens on the scores would outgrow the keys and are computed twice instead
-// (pa_weigh_tc.cu).
+// and head beside 34 (4-bit, 64 dims) to 512 bytes of keys, mostly stay in L2.  From
+// kWeighAgain new tokens on they are computed twice instead (pa_weigh_tc.cu): kept, those of
+// 16 new tokens of one head take 128 bytes a token, written and read, beside a 4-bit key's 68.
+// Both forms, us (kept, twice; head_dim 128, 16 sequences of up to 8192 tokens unless it says
+// otherwise): 2 new tokens of 4 heads per KV head 24 and 93; 8 of 4, 4 bits 57 and 94, 16 bits
+// 65 and 95; 15 of 4, 117 and 109, 121 and 98, of 256 dims (8 sequences) 73 and 96; a window of
+// 32 of 4 (4 sequences, 16 bits) 100 and 36.  The rule does not ask for heads: with many of them
+// twice comes out ahead earlier (4 new tokens of 16 heads 52 and 38, 16 bits 52 and 31; 8 of 8
+// 67 and 61, 69 and 54; 8 sequences, 8 of 16, 59 and 34, 59 and 24).
 //
 // Tokens are the M side of mma.sync, 8 query rows an N tile; a lane's 16 bytes of 8
 // consecutive dims of a row (or the 8 codes of a word, see pa_q4_attn.cuh) take the places
 // of two K-steps' fragments.  Warps walk their own tiles through their own rings, filled
 // by cp.async; a lane keeps its own maximum and sum, and lanes and warps meet at the end.
-// Sums are fp32 in a fixed order: results do not depend on timing.
+// Sums are fp32 in a fixed order: results do not depend on timing (but in the slot of a token
+// that several sequences of a call hold).
 //
 // Measured: the newest tokens of 32 sequences of up to 8192 tokens, 32 heads on 8 of 128,
-// 4 bits, 37.5 us a call: scores 29 (73 MB of keys; 58% of the issue slots), weights 14 alone,
-// the launches partly behind one another.  A CTA per partition of 1280 tokens: of 512 45 us,
-// of 2816 42.
+// 4 bits, 34 to 38 us a call (by lengths): scores 29 (73 MB of keys; 58% of the issue slots),
+// weights 14 alone, the launches partly behind one another.  Cut for two waves of CTAs, five
+// partitions of up to 1664 tokens, 36.2 us; for one (2816) 40.9, for three (1152) 35.7, but 27.1
+// for 24.4 (2 new tokens of 16 sequences) and 69 for 64 (16-bit keys of 256 dims).
 #include <atomic>
 #include <type_traits>
 
@@ -49,7 +57,9 @@ struct KeyTile {
     }
 };
 
-// CTAs that share an SM, and ring stages: many rows compute longer on a tile.
+// CTAs that registers let share an SM, and ring stages: many rows compute longer on a tile.
+// (Shared memory holds as many over codes; over 16-bit keys three, and of head_dim 256 one up to
+// 16 rows, two above.)
 __host__ __device__ constexpr int ctas_of(int nt) { return nt <= 2 ? 4 : 3; }
 __host__ __device__ constexpr int stages_of(int nt) { return nt <= 2 ? 4 : 2; }
 

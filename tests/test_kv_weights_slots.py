@@ -114,3 +114,30 @@ def test_a_score_of_minus_infinity_counts_as_nothing(pa, dtype, Q, G):  # noqa: 
     _, tol = q4.weigh_reference(q, gone, ks, tables, n, 0.1, w, 1.0)  # (a far key's size is no error of the others')
     x, r, t = (slots(y, tables, 0, L) for y in (got.double(), ref, tol))
     assert status == 0 and ((x - r).abs() <= t).all()
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_steps_without_a_call(pa, bits):  # noqa: F811
+    """A call at every third step, for the newest query alone; tokens of the steps between start from slots that
+    are cleared as they are appended, whatever those held."""
+    D, bs, KV, G, first, steps = 64, 16, 2, 3, (40, 7), 12
+    S, H = 2, 6
+    lens = [x + steps for x in first]
+    q, kc, ks, tables, _, w = inputs(lens, steps, G, KV, D, bs, F16, bits, 7)
+    dev = torch.full(w.shape, math.nan, device="cuda")
+    c, t, scales = kc.cuda(), tables.cuda(), ks.cuda() if ks is not None else None
+    ws = pa.alloc_weights_workspace(S, H, tables.shape[1] * bs)
+    ref = off = torch.zeros(w.shape, dtype=torch.float64)
+    for step in range(steps):
+        n = torch.tensor([x + step + 1 for x in first], dtype=torch.int32)
+        p = (n.cuda() - 1).long()
+        dev[t[torch.arange(S, device="cuda"), p // bs].long(), :, p % bs] = 0
+        if step % 3:
+            continue
+        pa.pa_kv_weights(q[:, step].contiguous().cuda(), c, t, n.cuda(), 0.125, dev, ws, k_scales=scales,
+                         decay=0.0 if step == 0 else 1.0)
+        got, tol = q4.weigh_reference(q[:, step:step + 1], kc, ks, tables, n, 0.125, torch.zeros(w.shape), 0.0)
+        ref, off = ref + got, off + tol
+    for b in range(S):
+        x, r, tol = (slots(y, tables, b, lens[b]) for y in (dev.cpu().double(), ref, off))
+        assert ((x - r).abs() <= tol + steps * 2.0 ** -23 * r).all()

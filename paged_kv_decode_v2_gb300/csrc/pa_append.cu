@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : MANY ? 3 : 4)
             if (!placed) {
                 placed = true;
                 int b, pos, angle;
-                if (!place_of(p, t, lane, false, &b, &pos, &angle))
+                if (!place_of<false>(p, t, lane, false, &b, &pos, &angle))
                     return;
                 if (p.rotary_dim)
                     load_angles(p.cos_sin + (size_t)angle * p.rotary_dim, rot, p.rotary_dim,

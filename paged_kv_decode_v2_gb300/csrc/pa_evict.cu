@@ -20,8 +20,9 @@
 // Rows written in a stretch lie below every row read later.
 //
 // Measured: 32 sequences of up to 8192 tokens (16 bits, 8 heads of 128) cut to 2048 into
-// other blocks 94 us: choosing 17, moving 74 (5.9 TB/s).  One of 100,000 tokens (4 bits, 4
-// heads) cut to 32,768: choosing 28 (a CTA per head 97), moving 12.
+// other blocks 92 to 94 us: choosing 17, moving 74 (5.9 TB/s).  One of 100,000 tokens (4 bits,
+// 4 heads) cut to 32,768: choosing 28 (a CTA per head 97), moving 12.  The same in place, single
+// calls behind a flush of L2 (to other blocks 102 and 44): 199 and 90, by the barriered steps.
 #include <cooperative_groups.h>
 
 #include <atomic>

@@ -37,9 +37,10 @@
 // CTAs of a sequence through the merge pass (V2) or distributed shared memory (V1 over a
 // cluster).
 //
-// Measured (head_dim 128): 32 sequences of up to 8192 tokens, 32 heads on 8, 43 us a call
-// (143 MB: 3.3 TB/s); 64 ragged ones, 64 heads on 8, 56 us (3.9 TB/s); one of 100,000
-// tokens, 32 on 4, 22 us; one of 1000 tokens 6 us.  The loop issues in 56 to 59% of its
+// Measured (head_dim 128): 32 sequences of up to 8192 tokens, 32 heads on 8, 39 to 43 us a
+// call by their lengths (143 MB: 3.5 TB/s); 64 ragged ones, 64 heads on 8, 56 to 68 us (3.2 to
+// 3.9 TB/s); one of 100,000 tokens, 32 on 4, 22 us; one of 1000 tokens 6 us.  16 rows per KV
+// head of such 32 sequences 60 us, 17 rows 93, 32 rows 97 (the 8-bit attention: 52, 59 and 60).  The loop issues in 56 to 59% of its
 // slots, 330 warp instructions for 16 tokens: conversions, scales and their products, not
 // DRAM, are what is left, and where calls are short some 5 us of set-up, merge and launches.
 #pragma once

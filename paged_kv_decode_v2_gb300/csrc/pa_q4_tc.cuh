@@ -28,7 +28,8 @@
 // rows stores only those of Q (see pa_tc.cuh), and its other row warps sleep.
 //
 // Measured (head_dim 128, 8 KV heads): 16 new tokens of 4 heads each for 32 sequences of up
-// to 8192 tokens 104 us (143 MB at 1.4 TB/s; mma.sync 165), 128 rows per KV head 128 (298).
+// to 8192 tokens 102 to 112 us by their lengths (143 MB at 1.4 TB/s; mma.sync 165; the 8-bit
+// attention 79), 128 rows per KV head 128 (298).
 // Some 2770 warp instructions for a tile of 64 tokens, two fifths of them the converters',
 // at 44% of the issue slots: a tile takes its CTA some 2800 clocks, of which the converters
 // work some 2200, and the thread that issues MMAs 1200.  Tried and slower: codes through a

@@ -14,7 +14,7 @@
 // pa_q4_tc.cuh: 0 below 2^-27 of that scale).  Keys are read twice, from L2 where they fit.
 //
 // Measured (32 new tokens, 32 heads on 8 of 128, 16-bit keys): 4 sequences of 4096 to 9216
-// tokens 38 us a call (scores kept or computed again by mma.sync: 100 and 87), of 16,384
+// tokens 34 to 39 us a call (scores kept or computed again by mma.sync: 100 and 87), of 16,384
 // 66 us (4.1 TB/s over both passes), of 128 tokens 12: long calls are bound by reading the
 // keys, short ones by two launches whose CTAs fetch Q, then keys, then totals.  One wave of
 // CTAs: 10 parts for 9.5 per sequence made 320 of them on 304 places, 82 us instead of 66.
